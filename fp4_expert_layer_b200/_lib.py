@@ -1,4 +1,4 @@
-"""ctypes binding of ``include/moe_layer.h`` (argument marshalling only).
+"""ctypes binding of ``include/moe_layer.h`` and ``include/moe_ops.h`` (argument marshalling only).
 
 Every step of the forward runs in the CUDA library; this module only converts
 numpy arrays / torch tensors into the pointers and sizes the C ABI takes.  If
@@ -27,7 +27,9 @@ OUT_DTYPE = {"f32": 0, "bf16": 1}
 EXPORTED = ["moe_layer_plan", "moe_admit", "moe_layer_create", "moe_set_slot_table", "moe_forward",
             "moe_forward_host", "moe_get_stats", "moe_destroy", "moe_last_error", "moe_debug_inject",
             "moe_profile_enable", "moe_profile_read", "moe_route_topk_noalloc", "moe_debug_read",
-            "moe_graph_capture", "moe_graph_launch", "moe_graph_destroy", "moe_set_policy", "moe_prefetch"]
+            "moe_graph_capture", "moe_graph_launch", "moe_graph_destroy", "moe_set_policy", "moe_prefetch",
+            "moe_fp4_quantize", "moe_fp4_dequantize", "moe_fp4_matmul", "moe_sort_tokens", "moe_dispatch",
+            "moe_dispatch_backward", "moe_combine", "moe_combine_backward"]
 POLICY = {"static": 0, "none": 1, "cache": 2, "hybrid": 3}
 
 
@@ -113,6 +115,15 @@ def lib():
         L.moe_route_topk_noalloc.argtypes = [C.c_void_p, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p,
                                              C.c_int32, C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p,
                                              C.c_void_p]
+        p, i32, i64 = C.c_void_p, C.c_int32, C.c_int64
+        L.moe_fp4_quantize.argtypes = [p, i32, i64, i64, i64, i32, i64, p, p, p, p]
+        L.moe_fp4_dequantize.argtypes = [p, p, p, i32, i64, i64, i64, p, i32, i64, p]
+        L.moe_fp4_matmul.argtypes = [p, p, p, i32, p, p, p, i32, i32, i32, i32, p, p, i32, i64, p]
+        L.moe_sort_tokens.argtypes = [p, i32, i32, i32, p, p, p, p, p]
+        L.moe_dispatch.argtypes = [p, i32, i32, i32, i32, i64, p, i32, p, i64, p]
+        L.moe_dispatch_backward.argtypes = [p, i32, i32, i32, i32, i32, i64, p, p, i64, p]
+        L.moe_combine.argtypes = [p, i32, i32, i32, i32, i32, i64, p, p, p, i32, i64, p]
+        L.moe_combine_backward.argtypes = [p, i32, i64, p, i32, i64, i32, i32, i32, i32, p, p, p, i64, p, p]
         for n in EXPORTED:
             f = getattr(L, n)
             if n not in ("moe_destroy", "moe_last_error"):

@@ -1,0 +1,617 @@
+// ops_matmul.cu -- grouped product of FP4 operands on tcgen05 block-scaled MMA.
+//
+//   y[r, n] = xG[r] wG[g] sum_k x[r, k] w[g, n, k],  r in [offsets[g], offsets[g+1])
+//
+// A work item is one token tile (up to NT rows of one group) and one block of 128
+// weight rows; weights are the A operand (M = 128), tokens the B operand (N = NT),
+// so that a small batch costs no more tensor work than its tile.  Codes arrive by
+// TMA (256 K elements, 128 bytes a row, a stage; 128-byte swizzle; a box may start
+// at any row, so ragged segments need no padding: what a box brings of the next
+// segment's rows ends in columns that are not stored).  Block scales stay in the
+// rows' own order in memory; two warps a stage read 128 rows' scales each with one
+// wide load a row and turn them over into the 512-byte blocks (32 rows x 4 row
+// groups x 4 scales) that tcgen05.cp moves to TMEM.
+//
+// Persistent, one CTA per SM; the item list is the scan of the groups' tile
+// counts, which every CTA makes for itself, so there is no workspace and no
+// counter.  With few items (SPLIT) a cluster of CTAs shares an item's K range and
+// adds the parts in rank order through distributed shared memory.
+//
+// Warp roles: 0 copies codes, 1 allocates TMEM and issues the MMAs, 2..5 read the
+// accumulators back and store, 6..9 bring the scales (pairs 6, 7 and 8, 9 on
+// alternate stages; the even one the weights', the odd one the tokens').  All
+// mbarrier waits are bounded.
+#include <cooperative_groups.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "ops_common.cuh"
+#include "tcgen05.cuh"
+#include "tma.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace moe {
+namespace {
+
+constexpr int kMmThreads = 320;
+constexpr int kMmMaxGroups = 1024;
+
+struct MatmulArgs {
+  CUtensorMap xmap, wmap;
+  const uint8_t *xs, *ws;        // block scales
+  const float *xG, *wG;          // NVFP4 only
+  const int *offsets;            // NULL: one group of all rows
+  void *y;
+  int64_t ldy;
+  int *err;
+  int rows, groups, N, K;
+  int nsf;                       // scales in a row
+  int sf_mode;                   // 0: a stage's scales in one load, 1: words of four, 2: bytes
+  int dtype;
+};
+
+template <int WF, int NT>
+struct MmGeom {
+  static constexpr int NBLK = (WF == WF_MX) ? 2 : 4;       // 4-scale blocks of 256 K
+  static constexpr int WORDS = NBLK;                       // 32-bit words of scales a row has in a stage
+  static constexpr int SF_BYTES = NBLK * 512;
+  static constexpr int A_BYTES = 128 * 128;
+  static constexpr int B_BYTES = NT * 128;
+  static constexpr int SF_OFF = A_BYTES + B_BYTES;
+  static constexpr int STAGE = (SF_OFF + 2 * SF_BYTES + 1023) / 1024 * 1024;
+  static constexpr int FIT = (205 * 1024) / STAGE;
+  static constexpr int NBUF = 2;
+  static constexpr int SF_COLS = 2 * NBLK * 4;             // TMEM columns a stage's scales take
+  static constexpr int SF_TMEM = NBUF * NT;
+  static constexpr int SF_FIT = (512 - SF_TMEM) / SF_COLS;
+  static constexpr int STAGES = FIT < 8 ? (FIT < SF_FIT ? FIT : SF_FIT) : (8 < SF_FIT ? 8 : SF_FIT);
+  static constexpr size_t SMEM = (size_t)STAGES * STAGE + 1024;
+  static_assert(STAGES >= 3, "a pipeline");
+  static_assert(SF_TMEM + STAGES * SF_COLS <= 512, "TMEM budget");
+  static_assert(SMEM + 17 * 1024 <= 227 * 1024, "shared-memory budget");
+};
+
+// Item -> group, first row, rows, weight row block.
+struct MmItem {
+  int g, row0, nrows, rb;
+};
+
+template <int NT>
+__device__ __forceinline__ MmItem mm_item(const MatmulArgs &a, long long item, int nrb, const long long *tpre,
+                                          const int *goff) {
+  const long long tile = item / nrb;
+  MmItem m;
+  m.rb = (int)(item - tile * nrb);
+  int lo = 0, hi = a.groups;                               // tpre[lo] <= tile < tpre[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tpre[mid] <= tile) lo = mid; else hi = mid;
+  }
+  m.g = lo;
+  const int begin = goff[2 * lo], end = goff[2 * lo + 1];
+  m.row0 = begin + (int)(tile - tpre[lo]) * NT;
+  m.nrows = min(NT, end - m.row0);
+  return m;
+}
+
+// The scales of one row for one stage (K elements 256 * it ..): WORDS words.
+// Columns past the row's end read as 1.0 (their codes are zero).
+template <int WORDS>
+__device__ __forceinline__ void load_sf(const uint8_t *row, int it, int nsf, int mode, uint32_t fill, uint32_t (&w)[WORDS]) {
+  const int c0 = it * WORDS * 4;
+  if (mode == 0) {
+    if constexpr (WORDS == 4) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row + c0));
+      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else {
+      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row + c0));
+      w[0] = v.x; w[1] = v.y;
+    }
+  } else if (mode == 1) {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i)
+      w[i] = c0 + 4 * i < nsf ? __ldg(reinterpret_cast<const uint32_t *>(row + c0 + 4 * i)) : fill;
+  } else {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+      w[i] = 0;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int c = c0 + 4 * i + b;
+        w[i] |= (c < nsf ? (uint32_t)__ldg(row + c) : (fill & 0xFFu)) << (8 * b);
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void store_out(void *y, int dtype, int64_t at, float v) {
+  if (dtype == MOE_DT_F32) static_cast<float *>(y)[at] = v;
+  else if (dtype == MOE_DT_BF16) static_cast<uint16_t *>(y)[at] = bf16_bits(v);
+  else static_cast<uint16_t *>(y)[at] = f16_bits(v);
+}
+
+template <int WF, int NT, bool SPLIT>
+__global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_constant__ MatmulArgs a) {
+  using Geo = MmGeom<WF, NT>;
+  constexpr int S = Geo::STAGES, NBUF = Geo::NBUF, WORDS = Geo::WORDS;
+  extern __shared__ __align__(1024) uint8_t mm_raw[];
+  __shared__ __align__(8) uint64_t full_bar[S];
+  __shared__ __align__(8) uint64_t empty_bar[S];
+  __shared__ __align__(8) uint64_t accf_bar[NBUF];
+  __shared__ __align__(8) uint64_t acce_bar[NBUF];
+  __shared__ __align__(8) uint64_t quiesce_bar;
+  __shared__ uint32_t tmem_base_s;
+  __shared__ long long tpre[kMmMaxGroups + 1];             // tiles before each group
+  __shared__ int goff[2 * kMmMaxGroups];                   // first row and end of each group
+  __shared__ long long wsum[kMmThreads / 32];
+  __shared__ int ok_s;
+
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(mm_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&full_bar[s]), 3);                // the codes' copies and two scale warps
+      mbar_init(smem_u32(&empty_bar[s]), 1);
+    }
+    for (int b = 0; b < NBUF; ++b) {
+      mbar_init(smem_u32(&accf_bar[b]), 1);
+      mbar_init(smem_u32(&acce_bar[b]), 4);
+    }
+    mbar_init(smem_u32(&quiesce_bar), 1);
+    ok_s = 1;
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_base_s), 512);
+    tmem_relinquish();
+  }
+  wait_prior_grid();
+  // tiles of each group, scanned: thread t takes `per` consecutive groups
+  {
+    const int per = (a.groups + kMmThreads - 1) / kMmThreads;
+    const int g0 = min(a.groups, tid * per), g1 = min(a.groups, g0 + per);
+    long long sum = 0;
+    for (int g = g0; g < g1; ++g) {
+      const int b = a.offsets ? min(max(__ldg(a.offsets + g), 0), a.rows) : 0;
+      const int e = a.offsets ? min(max(__ldg(a.offsets + g + 1), 0), a.rows) : a.rows;
+      goff[2 * g] = b;
+      goff[2 * g + 1] = max(b, e);
+      tpre[g] = sum;
+      sum += (max(b, e) - b + NT - 1) / NT;
+    }
+    long long inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    long long earlier = inc - sum, all = 0;
+    for (int w = 0; w < kMmThreads / 32; ++w) {
+      if (w < warp) earlier += wsum[w];
+      all += wsum[w];
+    }
+    for (int g = g0; g < g1; ++g) tpre[g] += earlier;
+    if (tid == 0) tpre[a.groups] = all;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_s;
+  const int nrb = (a.N + 127) / 128;
+  const long long n_items = tpre[a.groups] * nrb;
+  const int nk_all = (a.K + 255) / 256;
+
+  // SPLIT: cluster c takes item c and rank r of it the K range [k0, k1)
+  int ranks = 1, rank = 0;
+  if constexpr (SPLIT) {
+    ranks = (int)cg::this_cluster().num_blocks();
+    rank = (int)cg::this_cluster().block_rank();
+  }
+  const int k0 = nk_all * rank / ranks, k1 = nk_all * (rank + 1) / ranks;
+  const long long first = SPLIT ? blockIdx.x / ranks : blockIdx.x;
+  const long long step = SPLIT ? n_items + 1 : gridDim.x;  // one item at most when split
+
+  if (warp == 0) {
+    // ---------------- codes
+    int s = 0, issued = 0;
+    uint32_t ph = 0;
+    bool failed = false;
+    for (long long item = first; item < n_items && !failed; item += step) {
+      const MmItem m = mm_item<NT>(a, item, nrb, tpre, goff);
+      for (int it = k0; it < k1; ++it) {
+        if (issued >= S && !mbar_wait_warp(smem_u32(&empty_bar[s]), ph ^ 1u, a.err, 61)) { failed = true; break; }
+        const uint32_t bar = smem_u32(&full_bar[s]);
+        const uint32_t st = smem_u32(smem + (size_t)s * Geo::STAGE);
+        if (elect_one()) {
+          mbar_arrive_expect_tx(bar, (uint32_t)(Geo::A_BYTES + Geo::B_BYTES));
+          tma_load_3d(st, &a.wmap, bar, it * 128, m.rb * 128, m.g);
+          tma_load_2d(st + Geo::A_BYTES, &a.xmap, bar, it * 128, m.row0);
+        }
+        __syncwarp();
+        ++issued;
+        if (++s == S) { s = 0; ph ^= 1u; }
+      }
+    }
+    // every copy has landed before the CTA leaves (a stage whose scales never
+    // came keeps its phase: the wait then ends by its limit)
+    if (lane == 0) {
+      int s2 = 0;
+      uint32_t ph2 = 0;
+      for (int i = 0; i < issued; ++i) {
+        if (i >= issued - S) mbar_drain(smem_u32(&full_bar[s2]), ph2);
+        if (++s2 == S) { s2 = 0; ph2 ^= 1u; }
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issue: the whole warp runs the loop, one lane issues
+    int s = 0, n = 0;
+    uint32_t ph = 0;
+    bool failed = false;
+    for (long long item = first; item < n_items && !failed; item += step) {
+      const int buf = n % NBUF;
+      if (n >= NBUF && !mbar_wait_warp(smem_u32(&acce_bar[buf]), ((n / NBUF) - 1) & 1, a.err, 62)) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + (uint32_t)(buf * NT);
+      for (int it = k0; it < k1; ++it) {
+        if (!mbar_wait_warp(smem_u32(&full_bar[s]), ph, a.err, 63)) { failed = true; break; }
+        tc_fence_after();
+        const uint32_t st = smem_u32(smem + (size_t)s * Geo::STAGE);
+        const uint32_t sf_t = tmem + (uint32_t)(Geo::SF_TMEM + s * Geo::SF_COLS);
+        if (elect_one()) {
+#pragma unroll
+          for (int b = 0; b < 2 * Geo::NBLK; ++b) tc_cp_sf_block(sf_t + 4 * b, st + Geo::SF_OFF + 512 * b);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {                    // K = 64 an MMA
+            const int blk = (WF == WF_MX) ? (k >> 1) : k;
+            const uint32_t byte = (WF == WF_MX) ? (uint32_t)(2 * (k & 1)) : 0u;
+            const uint64_t adesc = umma_desc(st + k * 32, 16, 1024, 2);
+            const uint64_t bdesc = umma_desc(st + Geo::A_BYTES + k * 32, 16, 1024, 2);
+            const uint32_t sfa = (sf_t + (uint32_t)(blk * 4)) | (byte << 30);
+            const uint32_t sfb = (sf_t + (uint32_t)((Geo::NBLK + blk) * 4)) | (byte << 30);
+            const uint32_t idesc = idesc_fp4_block(128, NT, WF == WF_MX, byte, byte);
+            const uint32_t accum = (it > k0 || k > 0) ? 1u : 0u;
+            if constexpr (WF == WF_MX) umma_mxf4(acc, adesc, bdesc, idesc, sfa, sfb, accum);
+            else umma_nvf4(acc, adesc, bdesc, idesc, sfa, sfb, accum);
+          }
+          tc_commit(smem_u32(&empty_bar[s]));
+        }
+        __syncwarp();
+        if (++s == S) { s = 0; ph ^= 1u; }
+      }
+      if (failed) break;
+      if (elect_one()) tc_commit(smem_u32(&accf_bar[buf]));
+      __syncwarp();
+      ++n;
+    }
+    // every MMA has completed before TMEM is freed (and, when split, before the
+    // cluster meets), also when a wait gave up
+    __syncwarp();
+    if (elect_one()) tc_commit(smem_u32(&quiesce_bar));
+    __syncwarp();
+    mbar_drain(smem_u32(&quiesce_bar), 0);
+    if (failed && lane == 0) ok_s = 0;
+  } else if (warp < 6) {
+    // ---------------- accumulators to y: warp w has TMEM lanes 32 * (w % 4) ..
+    if constexpr (!SPLIT) {
+      const int quad = warp & 3;
+      int n = 0;
+      for (long long item = first; item < n_items; item += step) {
+        const MmItem m = mm_item<NT>(a, item, nrb, tpre, goff);
+        const int buf = n % NBUF;
+        if (!mbar_wait_warp(smem_u32(&accf_bar[buf]), (n / NBUF) & 1, a.err, 64)) break;
+        tc_fence_after();
+        const uint32_t acc = tmem + (uint32_t)(buf * NT) + ((uint32_t)(32 * quad) << 16);
+        const int col = m.rb * 128 + 32 * quad + lane;
+        const float wG = (WF == WF_NV) ? __ldg(a.wG + m.g) : 1.0f;
+#pragma unroll 1
+        for (int c0 = 0; c0 < m.nrows; c0 += 16) {
+          uint32_t d[16];
+          tmem_ld16(acc + (uint32_t)c0, d);
+          const float xG = (WF == WF_NV && c0 + lane < m.nrows && lane < 16) ? __ldg(a.xG + m.row0 + c0 + lane) : 1.0f;
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float sc = (WF == WF_NV) ? wG * __shfl_sync(0xffffffffu, xG, j) : 1.0f;
+            if (c0 + j < m.nrows && col < a.N)
+              store_out(a.y, a.dtype, (int64_t)(m.row0 + c0 + j) * a.ldy + col, __uint_as_float(d[j]) * sc);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&acce_bar[buf]));
+        ++n;
+      }
+    }
+  } else {
+    // ---------------- scales: pair p = (warp - 6) / 2 takes the stages with
+    // (stage count) % 2 == p.  Row words are loaded one stage of the pair ahead.
+    const int pair = (warp - 6) >> 1;
+    const bool tokens = (warp & 1) != 0;
+    const uint32_t fill = (WF == WF_MX) ? 0x7F7F7F7Fu : 0x38383838u;
+    constexpr int RG = (NT + 31) / 32 < 4 ? (NT + 31) / 32 : 4;        // 32-row groups of a token tile
+    // the (item, stage) sequence this warp loads, and where it stores
+    long long item = first;
+    int it = k0, seq = 0;
+    bool have = item < n_items && k1 > k0;
+    MmItem m{};
+    const uint8_t *rowp[4];
+    auto rows_of = [&]() {
+      m = mm_item<NT>(a, item, nrb, tpre, goff);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (tokens) {
+          const int r = min(m.row0 + 32 * j + lane, a.rows - 1);
+          rowp[j] = a.xs + (size_t)r * a.nsf;
+        } else {
+          const int r = min(m.rb * 128 + 32 * j + lane, a.N - 1);
+          rowp[j] = a.ws + ((size_t)m.g * a.N + r) * a.nsf;
+        }
+      }
+    };
+    if (have) rows_of();
+    auto advance = [&]() {
+      ++seq;
+      if (++it == k1) {
+        it = k0;
+        item += step;
+        have = item < n_items;
+        if (have) rows_of();
+      }
+    };
+    uint32_t cur[4][WORDS];
+    auto fetch = [&]() {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (!tokens || j < RG) {
+          load_sf<WORDS>(rowp[j], it, a.nsf, a.sf_mode, fill, cur[j]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < WORDS; ++i) cur[j][i] = fill;
+        }
+      }
+    };
+    if (pair == 1 && have) advance();
+    bool loaded = have;
+    if (have) fetch();
+    while (loaded) {
+      const int s = seq % S;
+      const int round = seq / S;
+      uint32_t hold[4][WORDS];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) hold[j][i] = cur[j][i];
+      advance();                                           // past the other pair's stage, to the next of this one
+      if (have) advance();
+      loaded = have;
+      if (have) fetch();
+      if (round > 0 && !mbar_wait_warp(smem_u32(&empty_bar[s]), (round - 1) & 1, a.err, 65)) break;
+      const uint32_t dst = smem_u32(smem + (size_t)s * Geo::STAGE) + Geo::SF_OFF + (tokens ? Geo::SF_BYTES : 0) + 16 * lane;
+#pragma unroll
+      for (int b = 0; b < WORDS; ++b)
+        sts128(dst + 512 * b, make_uint4(hold[0][b], hold[1][b], hold[2][b], hold[3][b]));
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&full_bar[s]));
+    }
+  }
+
+  if constexpr (SPLIT) {
+    // parts meet: rank q finishes weight rows [128 q / ranks, 128 (q + 1) / ranks)
+    cg::cluster_group cluster = cg::this_cluster();
+    float *recv = reinterpret_cast<float *>(smem);         // [source][rows of a rank][NT], over the stages
+    const bool any = first < n_items;                      // the same for the whole cluster
+    if (any && warp >= 2 && warp < 6) {
+      if (!mbar_wait_warp(smem_u32(&accf_bar[0]), 0, a.err, 66) && lane == 0) ok_s = 0;
+    }
+    __syncwarp();
+    tc_fence_before();
+    cluster.sync();                                        // every rank is done with its stages
+    const int per = 128 / ranks;                           // ranks is a power of two
+    if (any && warp >= 2 && warp < 6) {
+      tc_fence_after();
+      const int quad = warp & 3, row = 32 * quad + lane;
+      float *dst = cluster.map_shared_rank(recv, row / per) + ((size_t)rank * per + row % per) * NT;
+      const bool ok = ok_s != 0 && k1 > k0;                // a rank without stages adds nothing
+#pragma unroll 1
+      for (int c0 = 0; c0 < NT; c0 += 16) {
+        uint32_t v[16];
+        tmem_ld16(tmem + (uint32_t)c0 + ((uint32_t)(32 * quad) << 16), v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; j += 4)
+          *reinterpret_cast<float4 *>(dst + c0 + j) =
+              ok ? make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]), __uint_as_float(v[j + 2]),
+                               __uint_as_float(v[j + 3]))
+                 : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+    cluster.sync();                                        // every part is where it is added
+    if (any) {
+      const MmItem m = mm_item<NT>(a, first, nrb, tpre, goff);
+      const float wG = (WF == WF_NV) ? __ldg(a.wG + m.g) : 1.0f;
+      for (int i = tid; i < per * m.nrows; i += kMmThreads) {
+        const int c = i / per, r = i - c * per;            // neighbouring threads: neighbouring columns of y
+        float v = 0.0f;
+        for (int q = 0; q < ranks; ++q) v += recv[((size_t)q * per + r) * NT + c];
+        const int col = m.rb * 128 + rank * per + r;
+        const float sc = (WF == WF_NV) ? wG * __ldg(a.xG + m.row0 + c) : 1.0f;
+        if (col < a.N) store_out(a.y, a.dtype, (int64_t)(m.row0 + c) * a.ldy + col, v * sc);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+// Error word of this device's products: mapped host memory, which the bounded
+// waits write to when they give up and the next call reads.  Made once per device.
+moe_status_t matmul_error_word(const char *fn, ErrWord **out) {
+  static std::mutex mu;
+  static ErrWord *words[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= 64) return ops_fail(MOE_ERR_CUDA, fn, "no current device");
+  std::lock_guard<std::mutex> lock(mu);
+  if (!words[dev]) {
+    // also inside a stream capture: pinned host memory takes no part in it
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    void *p = nullptr;
+    e = cudaHostAlloc(&p, sizeof(ErrWord), cudaHostAllocMapped | cudaHostAllocPortable);
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return ops_fail(MOE_ERR_OOM, fn, "no pinned host memory for the error word");
+    }
+    words[dev] = static_cast<ErrWord *>(p);
+    *words[dev] = ErrWord{0, 0, nullptr};
+  }
+  *out = words[dev];
+  return MOE_OK;
+}
+
+template <int WF, int NT, bool SPLIT>
+cudaError_t launch_matmul(const MatmulArgs &a, int grid, int ranks, cudaStream_t s) {
+  using Geo = MmGeom<WF, NT>;
+  auto fn = fp4_matmul_kernel<WF, NT, SPLIT>;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Geo::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(grid * ranks));
+  cfg.blockDim = dim3(kMmThreads);
+  cfg.dynamicSmemBytes = Geo::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)ranks;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = SPLIT ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, fn, a);
+}
+
+template <int WF>
+cudaError_t run_matmul(const MatmulArgs &a, int nt, int grid, int ranks, cudaStream_t s) {
+  if (ranks > 1) {
+    if (nt == 16) return launch_matmul<WF, 16, true>(a, grid, ranks, s);
+    if (nt == 32) return launch_matmul<WF, 32, true>(a, grid, ranks, s);
+    if (nt == 64) return launch_matmul<WF, 64, true>(a, grid, ranks, s);
+    return launch_matmul<WF, 128, true>(a, grid, ranks, s);
+  }
+  if (nt == 16) return launch_matmul<WF, 16, false>(a, grid, 1, s);
+  if (nt == 32) return launch_matmul<WF, 32, false>(a, grid, 1, s);
+  if (nt == 64) return launch_matmul<WF, 64, false>(a, grid, 1, s);
+  return launch_matmul<WF, 128, false>(a, grid, 1, s);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_scales, const float *x_global,
+                                       int32_t rows, const uint8_t *w_codes, const uint8_t *w_scales,
+                                       const float *w_global, int32_t n_groups, int32_t N, int32_t K, int32_t fmt,
+                                       const int32_t *offsets, void *y, int32_t dtype, int64_t ldy, void *stream) {
+  static const char fn[] = "moe_fp4_matmul";
+  if (fmt != MOE_FMT_MXFP4 && fmt != MOE_FMT_NVFP4) return ops_invalid(fn, "fmt must be MOE_FMT_MXFP4 or MOE_FMT_NVFP4");
+  if (!is_float_dtype(dtype)) return ops_invalid(fn, "dtype must be F32, BF16 or F16");
+  if (rows < 0 || N < 1 || K < 32 || K % 32) return ops_invalid(fn, "need rows >= 0, N >= 1 and K a multiple of 32");
+  if (n_groups < 1 || n_groups > kMmMaxGroups || (int64_t)n_groups * N >= (int64_t)1 << 31)
+    return ops_invalid(fn, "need 1 <= n_groups <= 1024 and n_groups * N below 2^31");
+  if (!offsets && n_groups != 1) return ops_invalid(fn, "more than one group needs offsets");
+  if (ldy < N) return ops_invalid(fn, "ldy must be at least N");
+  if (rows == 0) return MOE_OK;
+  if (!x_codes || !x_scales || !w_codes || !w_scales || !y) return ops_invalid(fn, "operands and y must be device pointers");
+  if (fmt == MOE_FMT_NVFP4 && (!x_global || !w_global)) return ops_invalid(fn, "NVFP4 needs both global scales");
+  if (!aligned_to(x_codes, 16) || !aligned_to(w_codes, 16)) return ops_invalid(fn, "codes must be 16-byte aligned");
+  if (!aligned_to(y, dtype_bytes(dtype)) || !aligned_to(offsets, 4) || !aligned_to(x_global, 4) ||
+      !aligned_to(w_global, 4))
+    return ops_invalid(fn, "y, offsets and global scales must be aligned to their type");
+
+  MatmulArgs a{};
+  auto enc = map_encoder();
+  if (!enc) return ops_fail(MOE_ERR_CUDA, fn, "cuTensorMapEncodeTiled is unavailable");
+  // rows a group can be expected to have decide the token tile: the least tile
+  // that holds them, so that a decode batch streams weights and little else
+  const int64_t mean = (rows + n_groups - 1) / n_groups;
+  const int nt = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 128;
+  const cuuint64_t kb = (cuuint64_t)(K / 2);
+  const cuuint32_t ones[3] = {1, 1, 1};
+  {
+    const cuuint64_t dims[2] = {kb, (cuuint64_t)rows}, strides[1] = {kb};
+    const cuuint32_t box[2] = {128, (cuuint32_t)nt};
+    if (enc(&a.xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(x_codes), dims, strides, box, ones,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return ops_fail(MOE_ERR_CUDA, fn, "cuTensorMapEncodeTiled failed for x");
+  }
+  {
+    const cuuint64_t dims[3] = {kb, (cuuint64_t)N, (cuuint64_t)n_groups}, strides[2] = {kb, kb * (cuuint64_t)N};
+    const cuuint32_t box[3] = {128, 128, 1};
+    if (enc(&a.wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t *>(w_codes), dims, strides, box, ones,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return ops_fail(MOE_ERR_CUDA, fn, "cuTensorMapEncodeTiled failed for w");
+  }
+  ErrWord *err = nullptr;
+  const moe_status_t st = matmul_error_word(fn, &err);
+  if (st != MOE_OK) return st;
+  if (const int code = *(volatile int *)&err->code) {
+    *(volatile int *)&err->code = 0;
+    return ops_fail(MOE_ERR_CUDA, fn, "a device-side wait of an earlier call gave up (code " + std::to_string(code) + ")");
+  }
+  a.xs = x_scales; a.ws = w_scales;
+  a.xG = x_global; a.wG = w_global;
+  a.offsets = offsets;
+  a.y = y; a.ldy = ldy;
+  a.err = &err->code;
+  a.rows = rows; a.groups = n_groups; a.N = N; a.K = K;
+  a.nsf = K / (fmt == MOE_FMT_MXFP4 ? 32 : 16);
+  a.dtype = dtype;
+  const int stage = fmt == MOE_FMT_MXFP4 ? 8 : 16;         // scale bytes of 256 K
+  a.sf_mode = a.nsf % stage == 0 && aligned_to(x_scales, stage) && aligned_to(w_scales, stage) ? 0
+              : a.nsf % 4 == 0 && aligned_to(x_scales, 4) && aligned_to(w_scales, 4)           ? 1
+                                                                                              : 2;
+  // items there can be at most, and the ways to split K when they leave SMs idle:
+  // each way keeps at least two stages
+  const int sms = sm_count();
+  const int64_t nrb = (N + 127) / 128;
+  const int64_t tiles = std::min<int64_t>(rows, rows / nt + n_groups);
+  const int64_t items = tiles * nrb;
+  const int nk = (K + 255) / 256;
+  int ranks = 1;
+  while (ranks < 8 && items * ranks * 2 <= sms && nk >= 4 * ranks) ranks *= 2;
+  const int grid = (int)std::min<int64_t>(items, ranks > 1 ? items : sms);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = fmt == MOE_FMT_MXFP4 ? run_matmul<WF_MX>(a, nt, grid, ranks, s)
+                                             : run_matmul<WF_NV>(a, nt, grid, ranks, s);
+  return ops_launched(fn, e);
+}

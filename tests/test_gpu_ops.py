@@ -1,0 +1,630 @@
+"""The stand-alone operators on the GPU against their definitions in 64 bits.
+
+Tolerances.  A result that is rounded once to a type t may be off by
+eps(t)/2 of its value (plus half of t's smallest step near zero).  An fp32 sum
+of n terms in any order is within n * 2^-24 of the sum of the terms' magnitudes
+when each addition rounds to nearest; the tensor core's additions may cut off
+instead, 2^-23 each.  Quantisation, sorting and copies are exact.
+"""
+import numpy as np
+import pytest
+
+from tests import _gpu as G
+from tests import _ops_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+TINY = {"f32": 2.0 ** -149, "bf16": 2.0 ** -133, "f16": 2.0 ** -24}
+
+
+def dt(name):
+    t = G.torch()
+    return {"f32": t.float32, "bf16": t.bfloat16, "f16": t.float16}[name]
+
+
+def rounding(name, value):
+    """Half a step of a type at `value`."""
+    return G.torch().finfo(dt(name)).eps / 2 * np.abs(value) + TINY[name] / 2
+
+
+def f64(x):
+    return x.detach().cpu().double().numpy()
+
+
+def randn(shape, seed, dtype="f32", scale=1.0):
+    t = G.torch()
+    g = t.Generator().manual_seed(seed)
+    return (t.randn(shape, generator=g) * scale).to(dt(dtype)).cuda()
+
+
+def placed(x, pad, shift):
+    """The same 2-D values in a buffer with `pad` more elements a row, from element `shift` on."""
+    t = G.torch()
+    n, H = x.shape
+    buf = t.zeros(shift + n * (H + pad), dtype=x.dtype, device=x.device)
+    v = buf[shift:].view(n, H + pad)[:, :H]
+    v.copy_(x)
+    return v
+
+
+def ids_of(T, k, E, seed, low=0, high=None):
+    t = G.torch()
+    g = t.Generator().manual_seed(seed)
+    return t.randint(low, E if high is None else high, (T, k), generator=g, dtype=t.int32).cuda()
+
+
+# ----------------------------------------------------------------------- sort
+@pytest.mark.parametrize("T, k, E, low, high", [
+    (1, 1, 1, 0, 1), (1, 8, 64, 0, 64), (3, 32, 1024, 0, 1024), (33, 8, 64, -1, 66), (257, 5, 7, 0, 7),
+    (1000, 6, 257, -3, 260), (4097, 4, 1024, 0, 1024), (8192, 10, 512, 0, 514), (70001, 3, 100, -1, 100),
+    (50, 2, 8, -5, 0), (50, 2, 8, 8, 20), (999, 7, 16, 3, 4),
+])
+def test_sort_tokens(T, k, E, low, high):
+    F = G.library()
+    ids = ids_of(T, k, E, T + k, low, high)
+    r = F.sort_tokens(ids, E)
+    for name, want in zip(("counts", "offsets", "perm", "inv"), ref.sort_pairs(ids.cpu().numpy(), E)):
+        assert np.array_equal(r[name].cpu().numpy(), want), name
+
+
+def test_sort_of_no_tokens_and_of_extreme_ids():
+    t, F = G.torch(), G.library()
+    r = F.sort_tokens(t.empty((0, 3), dtype=t.int32, device="cuda"), 5)
+    assert r["counts"].tolist() == [0] * 5 and r["offsets"].tolist() == [0] * 6 and r["inv"].shape == (0, 3)
+    ids = t.tensor([[2147483647, -2147483648], [4, 4], [5, 0]], dtype=t.int32, device="cuda")
+    r = F.sort_tokens(ids, 5)
+    assert r["inv"].tolist() == [[-1, -1], [1, 2], [-1, 0]] and r["perm"].tolist() == [5, 2, 3, -1, -1, -1]
+
+
+# ------------------------------------------------------- dispatch and combine
+ROWS = [  # T, k, E, sinks, H, pad, shift
+    (1, 1, 1, 0, 1, 0, 0), (2, 3, 4, 1, 7, 0, 0), (5, 8, 16, 0, 64, 0, 0), (33, 8, 64, 2, 2048, 0, 0),
+    (64, 2, 8, 1, 100, 4, 0), (17, 6, 32, 0, 255, 1, 1), (9, 4, 8, 0, 264, 8, 8), (300, 10, 128, 3, 520, 0, 0),
+    (12, 32, 40, 0, 2047, 0, 3), (7, 5, 9, 9, 4100, 0, 0),
+]
+
+
+def _rows_case(T, k, E, sinks, seed):
+    ids = ids_of(T, k, E, seed, 0, E + sinks)
+    return G.library().sort_tokens(ids, E)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "f16", "u8"])
+@pytest.mark.parametrize("case", ROWS)
+def test_dispatch_copies_and_leaves_other_rows(case, dtype):
+    t, F = G.torch(), G.library()
+    T, k, E, sinks, H, pad, shift = case
+    inv = _rows_case(T, k, E, sinks, 1)["inv"]
+    x = randn((T, H), 2)
+    x = (x * 50).to(t.uint8) if dtype == "u8" else x.to(dt(dtype))
+    x = placed(x, pad, shift)
+    for rows in {T * k, max(1, T * k - 3)}:               # a capacity below what is needed drops the rest
+        out = placed(t.full((rows, H), 77, dtype=x.dtype, device="cuda"), pad, shift)
+        got = F.dispatch(x, inv, out=out)
+        assert got is out
+        want = ref.dispatch(f64(x), inv.cpu().numpy(), np.full((rows, H), 77.0))
+        assert np.array_equal(f64(out), want)
+    fresh = F.dispatch(x, inv)
+    used = inv[inv >= 0].long()
+    assert t.equal(fresh[used], x[t.nonzero(inv >= 0)[:, 0]])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "f16"])
+@pytest.mark.parametrize("case", ROWS)
+def test_dispatch_backward(case, dtype):
+    F = G.library()
+    T, k, E, sinks, H, pad, shift = case
+    inv = _rows_case(T, k, E, sinks, 3)["inv"]
+    dxs = placed(randn((T * k, H), 4, dtype), pad, shift)
+    dx = F.dispatch_backward(dxs, inv)
+    want, mag = ref.combine(f64(dxs), inv.cpu().numpy(), np.ones((T, k)))
+    assert np.all(np.abs(f64(dx) - want) <= k * 2.0 ** -24 * mag + rounding(dtype, want) * (1 + k * 2.0 ** -24))
+
+
+@pytest.mark.parametrize("types", [("bf16", "bf16"), ("f32", "bf16"), ("f32", "f32"), ("f16", "f16"), ("bf16", "f32"),
+                                   ("f16", "bf16")])
+@pytest.mark.parametrize("case", ROWS)
+def test_combine_and_its_gradients(case, types):
+    t, F = G.torch(), G.library()
+    T, k, E, sinks, H, pad, shift = case
+    ti, to = types
+    inv = _rows_case(T, k, E, sinks, 5)["inv"]
+    ys = placed(randn((T * k, H), 6, ti), pad, shift)
+    gates = randn((T, k), 7).abs()
+    iv, yd, gd = inv.cpu().numpy(), f64(ys), f64(gates)
+    y = F.combine(ys, inv, gates, out_dtype=dt(to))
+    want, mag = ref.combine(yd, iv, gd)
+    # k products and additions, one multiply-add each: n = k roundings
+    assert y.dtype == dt(to)
+    assert np.all(np.abs(f64(y) - want) <= k * 2.0 ** -24 * mag + rounding(to, want) * (1 + k * 2.0 ** -24))
+    plain = F.combine(ys, inv, out_dtype=dt(to))
+    assert t.equal(plain, F.combine(ys, inv, t.ones_like(gates), out_dtype=dt(to)))
+    dy = placed(randn((T, H), 8, to), pad, shift)
+    before = placed(randn((T * k, H), 9, ti), pad, shift)
+    out = before.clone()
+    dys, dg = F.combine_backward(dy, ys, inv, gates, out=out)
+    w_dys, w_dg, s_dg = ref.combine_backward(f64(dy), yd, iv, gd, f64(before))
+    # gate * dy is one fp32 rounding before that to the type
+    assert np.all(np.abs(f64(dys) - w_dys) <= rounding(ti, w_dys) * (1 + 2.0 ** -23) + 2.0 ** -24 * np.abs(w_dys))
+    unnamed = np.setdiff1d(np.arange(T * k), iv[iv >= 0])
+    assert np.array_equal(f64(dys)[unnamed], f64(before)[unnamed])
+    assert np.all(np.abs(f64(dg) - w_dg) <= H * 2.0 ** -24 * s_dg + TINY["f32"])
+    assert np.all(f64(dg)[iv < 0] == 0)
+
+
+def test_combine_gradient_against_differences():
+    """Directional differences of <dy, combine(ys, gates)> in 64 bits."""
+    F = G.library()
+    T, k, E, H = 23, 4, 9, 96
+    inv = _rows_case(T, k, E, 2, 11)["inv"]
+    ys, gates, dy = randn((T * k, H), 12), randn((T, k), 13), randn((T, H), 14)
+    dys, dg = F.combine_backward(dy, ys, inv, gates, out=G.torch().zeros_like(ys))
+    iv = inv.cpu().numpy()
+    rng = np.random.default_rng(0)
+
+    def loss(a, b):
+        return float((f64(dy) * ref.combine(a, iv, b)[0]).sum())
+
+    u, v, h = rng.standard_normal(ys.shape), rng.standard_normal(gates.shape), 1e-3
+    got_y, got_g = float((f64(dys) * u).sum()), float((f64(dg) * v).sum())
+    # the loss is linear in each: central differences are exact up to 64-bit rounding (~1e-16 / h of the loss's
+    # terms); dys and dg carry fp32 roundings: 2^-24 of each element, and of H terms
+    near_y = (loss(f64(ys) + h * u, f64(gates)) - loss(f64(ys) - h * u, f64(gates))) / (2 * h)
+    near_g = (loss(f64(ys), f64(gates) + h * v) - loss(f64(ys), f64(gates) - h * v)) / (2 * h)
+    size = float(np.abs(f64(dy)).sum() * np.abs(f64(ys)).max() * np.abs(f64(gates)).max())
+    assert abs(got_y - near_y) <= 2.0 ** -23 * np.abs(f64(dys) * u).sum() + 1e-12 * size
+    s_dg = ref.combine_backward(f64(dy), f64(ys), iv, f64(gates), f64(ys))[2]
+    assert abs(got_g - near_g) <= H * 2.0 ** -24 * (s_dg * np.abs(v)).sum() + 1e-12 * size
+
+
+def test_dispatch_gradient_against_differences():
+    F = G.library()
+    T, k, E, H = 19, 3, 8, 40
+    inv = _rows_case(T, k, E, 1, 15)["inv"]
+    dxs = randn((T * k, H), 16)
+    dx = F.dispatch_backward(dxs, inv)
+    iv = inv.cpu().numpy()
+    x, u, h = f64(randn((T, H), 17)), f64(randn((T, H), 18)), 1e-3
+
+    def loss(a):
+        return float((f64(dxs) * ref.dispatch(a, iv, np.zeros((T * k, H)))).sum())
+
+    near = (loss(x + h * u) - loss(x - h * u)) / (2 * h)
+    mag = ref.combine(f64(dxs), iv, np.ones((T, k)))[1]
+    size = float(np.abs(f64(dxs)).sum() * np.abs(x).max())
+    assert abs(float((f64(dx) * u).sum()) - near) <= (k + 1) * 2.0 ** -24 * (mag * np.abs(u)).sum() + 1e-12 * size
+
+
+def test_dropped_pairs_and_unnamed_rows_do_not_leak():
+    t, F = G.torch(), G.library()
+    nan = float("nan")
+    inv = t.tensor([[0, -1], [-1, -1], [2, 9], [-7, 1]], dtype=t.int32, device="cuda")   # 9 is past the rows
+    ys = randn((4, 72), 19)
+    ys[3] = nan                                             # named by nobody
+    gates = t.tensor([[.5, nan], [nan, float("inf")], [.25, nan], [nan, 2.0]], device="cuda")
+    y = F.combine(ys, inv, gates)
+    assert t.isfinite(y).all() and (y[1] == 0).all()
+    assert t.equal(y[0], .5 * ys[0]) and t.equal(y[2], .25 * ys[2]) and t.equal(y[3], 2 * ys[1])
+    dy = randn((4, 72), 20)
+    dy[1] = nan                                             # a token with no pair left
+    out = t.full_like(ys, 5.0)
+    dys, dg = F.combine_backward(dy, ys, inv, gates, out=out)
+    assert t.isfinite(dys).all() and (dys[3] == 5).all() and t.isfinite(dg).all()
+    assert (dg[1] == 0).all() and dg[0, 1] == 0 and dg[2, 1] == 0 and dg[3, 0] == 0
+    dx = F.dispatch_backward(ys, inv)
+    assert t.isfinite(dx).all() and (dx[1] == 0).all()
+    xs = t.full((4, 72), 5.0, device="cuda")
+    F.dispatch(dy, inv, out=xs)
+    assert (xs[3] == 5).all() and t.isfinite(xs).all()
+
+
+def test_partial_gradients_of_combine():
+    """dys alone (ys not read) and dgates alone, through the C entry point."""
+    t, F = G.torch(), G.library()
+    T, k, H = 6, 2, 40
+    inv = _rows_case(T, k, 4, 0, 21)["inv"]
+    ys, dy, gates = randn((T * k, H), 22), randn((T, H), 23), randn((T, k), 24)
+    dys, dg = F.combine_backward(dy, ys, inv, gates)
+    s = t.cuda.current_stream().cuda_stream
+    a, b = t.zeros_like(dys), t.zeros_like(dg)
+    L = F.lib()
+    assert L.moe_combine_backward(dy.data_ptr(), 0, H, None, 0, H, T * k, T, k, H, inv.data_ptr(), gates.data_ptr(),
+                                  a.data_ptr(), H, None, s) == 0
+    assert L.moe_combine_backward(dy.data_ptr(), 0, H, ys.data_ptr(), 0, H, T * k, T, k, H, inv.data_ptr(),
+                                  gates.data_ptr(), None, H, b.data_ptr(), s) == 0
+    assert t.equal(a, dys) and t.equal(b, dg)
+
+
+# ----------------------------------------------------------------- quantise
+def _hard_rows(n, K, seed):
+    """Values of many sizes, on borders between codes, zeros and subnormals among them."""
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal((n, K)) * 2.0 ** rng.integers(-12, 12, (n, 1))
+    grid = rng.choice([0, .25, .5, .75, 1, 1.25, 1.75, 2.5, 3.5, 5, 6, 7], (n, K)) * rng.choice([-1, 1], (n, K))
+    d = rng.choice([1, 1.125, 1.25, 1.375, 1.5, 1.625, 1.75, 1.875], (n, K // 16)) * 2.0 ** rng.integers(-4, 4, (n, K // 16))
+    on = grid * np.repeat(d, 16, axis=1)
+    x = np.where(rng.random((n, 1)) < 0.5, x, on)
+    x[rng.random((n, K)) < 0.05] = 0
+    if n > 2:
+        x[1] = 0
+        x[2, :K // 2] = 0
+    return x
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "f16"])
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("n, K, per, pad, shift", [
+    (1, 32, 1, 0, 0), (3, 64, 1, 0, 0), (8, 2048, 1, 0, 0), (257, 96, 1, 0, 0), (5, 4128, 1, 8, 8), (4, 544, 1, 3, 1),
+    (2, 32800, 1, 0, 0), (64, 256, 16, 0, 0), (6, 160, 2, 0, 0), (1024, 2048, 1024, 0, 0), (12, 96, 4, 2, 2),
+    (700, 1024, 350, 0, 0),
+])
+def test_quantize_is_exact(dtype, fmt, n, K, per, pad, shift):
+    t, F = G.torch(), G.library()
+    x = placed(t.from_numpy(_hard_rows(n, K, n + K)).to(dt(dtype)).cuda(), pad, shift)
+    q = F.fp4_quantize(x, fmt, rows_per_scale=per)
+    codes, scales, Gs, vals = ref.quantize(f64(x), fmt, per)
+    assert np.array_equal(q.scales.cpu().numpy(), scales.reshape(n, -1))
+    if fmt == "nvfp4":
+        assert np.array_equal(f64(q.global_scale), Gs)
+    got = ref.values(q.codes.cpu().numpy(), q.scales.cpu().numpy(), Gs, fmt, per)
+    assert np.array_equal(got, vals)
+    assert np.array_equal(f64(F.fp4_dequantize(q)), vals)
+    back = F.fp4_dequantize(q, dtype=t.bfloat16)
+    assert np.array_equal(f64(back), f64(t.from_numpy(vals).float().to(t.bfloat16)))
+    again = F.FP4Tensor(*(None if p is None else t.empty_like(p) for p in q[:3]), fmt)
+    assert F.fp4_quantize(x, fmt, per, out=again) is again
+    assert all(a is None or t.equal(a, b) for a, b in zip(again[:3], q[:3]))
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("per", [1, 4])
+def test_quantize_at_the_ends_of_the_range(fmt, per):
+    """The largest and smallest floats, infinities, NaN; blocks that are not finite become NaN alone."""
+    t, F = G.torch(), G.library()
+    x = np.zeros((8, 128), dtype=np.float32)
+    x[0] = np.finfo(np.float32).max
+    x[1, ::3] = 2.0 ** -149
+    x[2, 5] = 2.0 ** -126
+    x[3] = np.linspace(-1, 1, 128)
+    x[3, 40] = np.nan
+    x[4] = np.linspace(-3, 3, 128)
+    x[4, 70], x[4, 90] = np.inf, -np.inf
+    x[5] = np.nan
+    x[6, :64] = 1e-30
+    x[6, 64:] = 1e30
+    x[7] = -0.0
+    q = F.fp4_quantize(t.from_numpy(x).cuda(), fmt, rows_per_scale=per)
+    codes, scales, Gs, vals = ref.quantize(x.astype(np.float64), fmt, per)
+    assert np.array_equal(q.scales.cpu().numpy(), scales.reshape(8, -1))
+    if fmt == "nvfp4":
+        assert np.array_equal(f64(q.global_scale), Gs)
+    with np.errstate(over="ignore"):
+        want = vals.astype(np.float32).astype(np.float64)
+    assert np.array_equal(f64(F.fp4_dequantize(q)), want, equal_nan=True)
+
+
+def test_quantize_matrices_at_once():
+    """A 3-D tensor: one global scale a matrix, as three calls would give."""
+    t, F = G.torch(), G.library()
+    w = randn((3, 40, 96), 30, "bf16", 0.02)
+    w[1] *= 100
+    q = F.fp4_quantize(w, "nvfp4")
+    assert q.codes.shape == (3, 40, 48) and q.scales.shape == (3, 40, 6) and q.global_scale.shape == (3,)
+    for e in range(3):
+        one = F.fp4_quantize(w[e], "nvfp4", rows_per_scale=40)
+        assert t.equal(q.codes[e], one.codes) and t.equal(q.scales[e], one.scales)
+        assert q.global_scale[e] == one.global_scale[0]
+    assert F.fp4_dequantize(q).shape == w.shape
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_dequantize_every_code(fmt):
+    t, F = G.torch(), G.library()
+    block = ref.BLOCK[fmt]
+    codes = np.tile(np.arange(256, dtype=np.uint8), block // 2)[: 256 * block // 2].reshape(256, block // 2)
+    if block == 16:                                        # K must be a multiple of 32: two blocks a row
+        codes = np.concatenate([codes, codes], 1)
+    scales = np.repeat(np.arange(256, dtype=np.uint8)[:, None], codes.shape[1] * 2 // block, axis=1)
+    Gs = np.full(256, 0.375, dtype=np.float32) if fmt == "nvfp4" else None
+    q = F.FP4Tensor(t.from_numpy(codes).cuda(), t.from_numpy(scales).cuda(),
+                    None if Gs is None else t.from_numpy(Gs).cuda(), fmt)
+    with np.errstate(over="ignore"):
+        want = ref.values(codes, scales, Gs, fmt).astype(np.float32)
+    assert np.array_equal(F.fp4_dequantize(q).cpu().numpy(), want, equal_nan=True)
+
+
+# ------------------------------------------------------------------- product
+def _operands(fmt, rows, E, N, K, seed):
+    """Random codes and scales of a few octaves (every code, every mantissa), on the GPU."""
+    t, F = G.torch(), G.library()
+    rng = np.random.default_rng(seed)
+
+    def one(lead, per):
+        codes = rng.integers(0, 256, lead + (K // 2,), dtype=np.uint8)
+        nb = lead + (K // ref.BLOCK[fmt],)
+        scales = rng.integers(124, 131, nb, dtype=np.uint8) if fmt == "mxfp4" else rng.integers(40, 72, nb, dtype=np.uint8)
+        n = int(np.prod(lead)) // per
+        g = None if fmt == "mxfp4" else t.from_numpy(rng.uniform(0.5, 2, n).astype(np.float32)).cuda()
+        return F.FP4Tensor(t.from_numpy(codes).cuda(), t.from_numpy(scales).cuda(), g, fmt)
+
+    return one((rows,), 1), one((E, N), N)
+
+
+def _wide(q, per):
+    c, s = q.codes.cpu().numpy(), q.scales.cpu().numpy()
+    g = None if q.global_scale is None else q.global_scale.cpu().numpy()
+    return ref.values(c.reshape(-1, c.shape[-1]), s.reshape(-1, s.shape[-1]), g, q.fmt, per)
+
+
+def _check_product(x, w, offsets, y0, y, out):
+    N, K = w.codes.shape[-2], 2 * w.codes.shape[-1]
+    E = w.codes.shape[0]
+    off = [0, x.codes.shape[0]] if offsets is None else offsets.tolist()
+    want, mag = ref.matmul(_wide(x, 1), _wide(w, N).reshape(E, N, K), off, f64(y0))
+    # products are exact; K additions that may cut off; the two scales' products round twice
+    tol = (K * 2.0 ** -23 + 2.0 ** -23) * mag * (1 + 2.0 ** -20) + rounding(out, want) * (1 + 2.0 ** -10)
+    err = np.abs(f64(y) - want)
+    assert np.all(err <= tol), f"worst {np.max(err - tol)} at {np.unravel_index(np.argmax(err - tol), err.shape)}"
+    a, b = off[0], off[-1]
+    keep = np.r_[0:a, b:want.shape[0]]
+    assert np.array_equal(f64(y)[keep], f64(y0)[keep])
+
+
+DENSE = [(1, 1, 32), (1, 4096, 4096), (2, 127, 96), (7, 128, 256), (16, 130, 288), (17, 256, 512), (33, 64, 2048),
+         (65, 384, 1056), (128, 129, 160), (129, 256, 320), (300, 200, 1024), (1000, 512, 768), (3, 2048, 8224)]
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("rows, N, K", DENSE)
+def test_dense_product(fmt, rows, N, K):
+    t, F = G.torch(), G.library()
+    x, w = _operands(fmt, rows, 1, N, K, rows + N + K)
+    for out in ("f32", "bf16", "f16"):
+        if out == "f16" and K > 1024:
+            continue                                       # sums pass fp16's range
+        y = F.fp4_matmul(x, w, out_dtype=dt(out))
+        _check_product(x, w, None, t.zeros_like(y), y, out)
+    flat = F.FP4Tensor(w.codes[0], w.scales[0], w.global_scale, fmt)
+    assert t.equal(F.fp4_matmul(x, flat, out_dtype=dt("f32")), F.fp4_matmul(x, w, out_dtype=dt("f32")))
+
+
+GROUPED = [  # segment lengths, rows behind, N, K
+    ([1], 0, 64, 64), ([0, 1, 0], 2, 128, 256), ([3, 0, 17, 16, 0, 1], 0, 200, 512), ([40, 5, 130, 0, 64], 3, 256, 288),
+    ([256, 1, 129, 300], 0, 129, 1024), ([0, 0], 5, 128, 64), ([2] * 64, 0, 512, 2048), ([1] * 100 + [0] * 24, 1, 130, 96),
+    ([0] * 1000 + [7] + [0] * 23, 0, 128, 128), ([700], 9, 320, 256),
+]
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("lens, behind, N, K", GROUPED)
+def test_grouped_product(fmt, lens, behind, N, K):
+    t, F = G.torch(), G.library()
+    rows, E = sum(lens) + behind, len(lens)
+    x, w = _operands(fmt, rows, E, N, K, rows + N + K)
+    off = t.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=t.int32, device="cuda")
+    for out, pad, shift in (("f32", 0, 0), ("bf16", 3, 1), ("f32", 8, 4)):
+        y0 = placed(randn((rows, N), 1, out), pad, shift)
+        y = placed(y0, pad, shift)
+        assert F.fp4_matmul(x, w, off, out=y) is y
+        _check_product(x, w, off, y0, y, out)
+        again = placed(y0, pad, shift)
+        F.fp4_matmul(x, w, off, out=again)
+        assert t.equal(y, again)
+
+
+def test_grouped_product_of_a_first_row_past_zero():
+    """offsets[0] > 0: the rows before the first segment stay as they are too."""
+    t, F = G.torch(), G.library()
+    x, w = _operands("nvfp4", 50, 3, 136, 160, 3)
+    off = t.tensor([5, 20, 20, 45], dtype=t.int32, device="cuda")
+    y0 = randn((50, 136), 2)
+    y = y0.clone()
+    F.fp4_matmul(x, w, off, out=y)
+    _check_product(x, w, off, y0, y, "f32")
+
+
+def test_offsets_out_of_range_are_cut_to_the_rows():
+    t, F = G.torch(), G.library()
+    x, w = _operands("mxfp4", 20, 3, 64, 64, 4)
+    y0 = randn((20, 64), 3)
+    wild, cut = ([-9, 6, 15, 1 << 30], [0, 6, 15, 20])
+    ys = []
+    for off in (wild, cut):
+        y = y0.clone()
+        F.fp4_matmul(x, w, t.tensor(off, dtype=t.int32, device="cuda"), out=y)
+        ys.append(y)
+    assert t.equal(*ys)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("shift", [0, 1, 4])
+def test_product_of_scales_that_are_not_aligned(fmt, shift):
+    t, F = G.torch(), G.library()
+    for rows, N, K in ((20, 130, 512), (5, 64, 128)):
+        x, w = _operands(fmt, rows, 1, N, K, 5)
+
+        def moved(s):
+            buf = t.empty(s.numel() + shift, dtype=t.uint8, device="cuda")
+            buf[shift:].copy_(s.flatten())
+            return buf[shift:].view(s.shape)
+
+        y = F.fp4_matmul(F.FP4Tensor(x.codes, moved(x.scales), x.global_scale, fmt),
+                         F.FP4Tensor(w.codes, moved(w.scales), w.global_scale, fmt), out_dtype=dt("f32"))
+        assert t.equal(y, F.fp4_matmul(x, w, out_dtype=dt("f32")))
+        _check_product(x, w, None, t.zeros_like(y), y, "f32")
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_nan_blocks_stay_in_their_rows(fmt):
+    """A NaN scale in a row of x is that row of y, one in a row of w that column, one
+    behind the segments nothing."""
+    t, F = G.torch(), G.library()
+    x, w = _operands(fmt, 40, 2, 72, 256, 6)
+    nan = 255 if fmt == "mxfp4" else 127
+    off = t.tensor([0, 17, 38], dtype=t.int32, device="cuda")
+    clean = F.fp4_matmul(x, w, off, out=t.zeros((40, 72), device="cuda"))
+    x.scales[16, 1] = nan
+    x.scales[39, 0] = nan
+    w.scales[1, 5, 2] = nan
+    y = F.fp4_matmul(x, w, off, out=t.zeros((40, 72), device="cuda"))
+    hit = t.zeros((40, 72), dtype=t.bool, device="cuda")
+    hit[16] = True
+    hit[17:38, 5] = True
+    assert t.isnan(y[hit]).all() and t.equal(y[~hit], clean[~hit])
+
+
+# ------------------------------------------------------- streams, graphs, use
+def _path(F, x, ids, gates, w1, w2, E, fmt):
+    t = G.torch()
+    r = F.sort_tokens(ids, E)
+    q = F.fp4_quantize(x, fmt)
+    parts = [F.dispatch(p, r["inv"]) for p in (q.codes, q.scales)]
+    gs = None if q.global_scale is None else F.dispatch(q.global_scale[:, None], r["inv"])[:, 0]
+    a = F.fp4_matmul(F.FP4Tensor(*parts, gs, fmt), w1, r["offsets"], out_dtype=t.float32)
+    gate, up = a.chunk(2, dim=1)
+    h = t.nn.functional.silu(gate) * up
+    ys = F.fp4_matmul(F.fp4_quantize(h, fmt), w2, r["offsets"], out_dtype=t.float32)
+    return F.combine(ys, r["inv"], gates, out_dtype=t.bfloat16), ys, r
+
+
+def _path_inputs(fmt, T, H, inter, E, k, seed=40):
+    F = G.library()
+    w1 = F.fp4_quantize(randn((E, 2 * inter, H), seed, "bf16", 0.05), fmt)
+    w2 = F.fp4_quantize(randn((E, H, inter), seed + 1, "bf16", 0.05), fmt)
+    return randn((T, H), seed + 2, "bf16"), ids_of(T, k, E, seed + 3), randn((T, k), seed + 4).abs(), w1, w2
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_graph_replays_the_path_and_streams_do_not_mix(fmt):
+    t, F = G.torch(), G.library()
+    E, k, H, inter = 16, 4, 512, 256
+    x, ids, gates, w1, w2 = _path_inputs(fmt, 60, H, inter, E, k)
+    want = _path(F, x, ids, gates, w1, w2, E, fmt)[0].clone()
+    x2, ids2, gates2 = randn(x.shape, 50, "bf16"), ids_of(60, k, E, 51), randn(gates.shape, 52).abs()
+    want2 = _path(F, x2, ids2, gates2, w1, w2, E, fmt)[0].clone()
+    bufs = [x.clone(), ids.clone(), gates.clone()]
+    graphs, outs = [], []
+    for _ in range(2):                                     # two graphs over the same inputs share no workspace
+        g = t.cuda.CUDAGraph()
+        with t.cuda.graph(g):
+            outs.append(_path(F, *bufs, w1, w2, E, fmt)[0])
+        graphs.append(g)
+    side = [t.cuda.Stream(), t.cuda.Stream()]
+    for inputs, expect in (((x2, ids2, gates2), want2), ((x, ids, gates), want)):
+        for b, v in zip(bufs, inputs):
+            b.copy_(v)
+        t.cuda.synchronize()
+        for rep in range(3):
+            for g, s in zip(graphs, side):
+                with t.cuda.stream(s):
+                    g.replay()
+        t.cuda.synchronize()
+        assert t.equal(outs[0], expect) and t.equal(outs[1], expect)
+    # calls given a stream, two at once
+    t.cuda.synchronize()
+    got = []
+    for s, (a, i, gt) in zip(side, ((x, ids, gates), (x2, ids2, gates2))):
+        r = F.sort_tokens(i, E, stream=s)
+        xs = F.dispatch(a, r["inv"], stream=s)
+        got.append((F.combine(xs, r["inv"], gt, stream=s.cuda_stream), r, a, gt))
+    t.cuda.synchronize()
+    for y, r, a, gt in got:
+        assert t.equal(y, F.combine(F.dispatch(a, r["inv"]), r["inv"], gt))
+
+
+def test_backward_in_a_graph():
+    t, F = G.torch(), G.library()
+    T, k, E, H = 40, 3, 8, 136
+    inv = _rows_case(T, k, E, 1, 60)["inv"]
+    ys, dy, gates = randn((T * k, H), 61), randn((T, H), 62), randn((T, k), 63)
+    keep = t.zeros_like(ys)
+    dys, dg = F.combine_backward(dy, ys, inv, gates, out=keep.clone())
+    dx = F.dispatch_backward(ys, inv)
+    g = t.cuda.CUDAGraph()
+    with t.cuda.graph(g):
+        dys2, dg2 = F.combine_backward(dy, ys, inv, gates, out=keep)
+        dx2 = F.dispatch_backward(ys, inv)
+    g.replay()
+    t.cuda.synchronize()
+    assert t.equal(dys, dys2) and t.equal(dg, dg2) and t.equal(dx, dx2)
+
+
+def test_path_equals_the_layers_own_a4_forward():
+    """Route, sort, quantise, dispatch, product, SwiGLU, quantise, product, combine:
+    the layer's A4 forward on the same weights, which fp4_quantize made.  Near a
+    border the two forms of silu can pick neighbouring codes of h; the tolerance is
+    the one the layer's own A4 test has for that."""
+    import synth
+    t, F = G.torch(), G.library()
+    from tests import _cases as cs
+    import oracle
+    wl = synth.custom_workload(512, 256, 16, 4)
+    lw = synth.make_layer(wl, seed=70)
+    E, H, inter = 16, 512, 256
+    mats = [randn((E, *s), 71 + i, "bf16", 0.05) for i, s in enumerate(((inter, H), (inter, H), (H, inter)))]
+    q = [F.fp4_quantize(m, "mxfp4") for m in mats]
+    for m in range(3):
+        lw.codes[m] = q[m].codes.cpu().numpy()
+        lw.scales[m] = q[m].scales.cpu().numpy()
+    L = oracle.Layer.from_weights(lw, numerics="a4")
+    x_bits, _ = cs.tokens_with_margin(L, wl, 130, stream=5)
+    layer = G.make_layer(lw, n_slots=E, max_tokens=130, numerics="a4")
+    y_layer, r = G.run(layer, x_bits)
+    layer.close()
+    x = G.to_device(x_bits)
+    ids = t.empty((130, 4), dtype=t.int32, device="cuda")
+    gates = t.empty((130, 4), dtype=t.float32, device="cuda")
+    F._lib.route_topk_noalloc(x, t.from_numpy(lw.router_w).cuda(),
+                              None if lw.router_bias is None else t.from_numpy(lw.router_bias).cuda(), 4, ids, gates)
+    w1 = F.FP4Tensor(t.cat([q[0].codes, q[1].codes], 1), t.cat([q[0].scales, q[1].scales], 1), None, "mxfp4")
+    y, _, s = _path(F, x, ids, gates, w1, q[2], E, "mxfp4")
+    assert np.array_equal(s["offsets"].cpu().numpy(), r["offsets"])
+    assert np.array_equal(s["inv"].cpu().numpy().reshape(-1), r["inv"])
+    y32 = F.combine(_, s["inv"], gates)
+    G.check_output(y32.cpu().numpy(), y_layer)
+    y_ref, *_r = L.forward(x_bits)
+    G.check_output(y32.cpu().numpy(), y_ref)
+
+
+def test_binding_refusals_on_the_gpu():
+    t, F = G.torch(), G.library()
+    x, w = _operands("nvfp4", 8, 2, 64, 64, 80)
+    off = t.tensor([0, 4, 8], dtype=t.int32, device="cuda")
+    xb = randn((8, 64), 1, "bf16")
+    inv = t.zeros((8, 2), dtype=t.int32, device="cuda")
+    bad = [
+        lambda: F.fp4_matmul(x, w),                                           # groups without offsets
+        lambda: F.fp4_matmul(x, w, off.long()),
+        lambda: F.fp4_matmul(x, w, off[:2]),
+        lambda: F.fp4_matmul(x, w, off.cpu()),
+        lambda: F.fp4_matmul(x, w, off, out_dtype=t.float64),
+        lambda: F.fp4_matmul(x, w, off, out=t.empty((8, 63), device="cuda")),
+        lambda: F.fp4_matmul(x._replace(fmt="mxfp4"), w, off),
+        lambda: F.fp4_matmul(x._replace(global_scale=None), w, off),
+        lambda: F.fp4_matmul(x._replace(scales=x.scales[:, :2]), w, off),
+        lambda: F.fp4_matmul(x._replace(codes=x.codes.t()), w, off),
+        lambda: F.fp4_quantize(xb, "fp8"),
+        lambda: F.fp4_quantize(xb.long()),
+        lambda: F.fp4_quantize(xb[:, :40]),
+        lambda: F.fp4_quantize(xb.t()),
+        lambda: F.fp4_quantize(xb, "nvfp4", rows_per_scale=3),
+        lambda: F.fp4_quantize(xb[:1].expand(8, 64)),                         # rows that are one row
+        lambda: F.fp4_quantize(xb, "nvfp4", out=x._replace(fmt="mxfp4", global_scale=None)),
+        lambda: F.sort_tokens(inv.long(), 4),
+        lambda: F.sort_tokens(inv, 0),
+        lambda: F.sort_tokens(inv, 1025),
+        lambda: F.dispatch(xb, inv[:4]),
+        lambda: F.dispatch(xb.double(), inv),
+        lambda: F.dispatch(xb, inv.t()),
+        lambda: F.dispatch(xb, inv.cpu()),
+        lambda: F.combine(xb, inv, t.ones((8, 3), device="cuda")),
+        lambda: F.combine(xb, inv, t.ones((8, 2), device="cuda").half()),
+        lambda: F.combine(xb.view(t.uint8), inv),
+        lambda: F.combine_backward(xb, xb[:, :32], inv),
+        lambda: F.dispatch_backward(xb, inv, out=t.empty((8, 64), device="cuda")),
+        lambda: F.dispatch(xb, inv, stream=t.cuda.Stream(), out=t.empty((16, 64))),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises(F.MoEError) as ei:
+            call()
+        assert ei.value.status == 1, i
