@@ -26,9 +26,7 @@
 
 #include <mutex>
 
-#include "ops_common.cuh"
-#include "tcgen05.cuh"
-#include "tma.cuh"
+#include "ops_matmul.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -36,21 +34,6 @@ namespace moe {
 namespace {
 
 constexpr int kMmThreads = 320;
-constexpr int kMmMaxGroups = 1024;
-
-struct MatmulArgs {
-  CUtensorMap xmap, wmap;
-  const uint8_t *xs, *ws;        // block scales
-  const float *xG, *wG;          // NVFP4 only
-  const int *offsets;            // NULL: one group of all rows
-  void *y;
-  int64_t ldy;
-  int *err;
-  int rows, groups, N, K;
-  int nsf;                       // scales in a row
-  int sf_mode;                   // 0: a stage's scales in one load, 1: words of four, 2: bytes
-  int dtype;
-};
 
 template <int WF, int NT>
 struct MmGeom {
@@ -73,65 +56,6 @@ struct MmGeom {
   static_assert(SMEM + 17 * 1024 <= 227 * 1024, "shared-memory budget");
 };
 
-// Item -> group, first row, rows, weight row block.
-struct MmItem {
-  int g, row0, nrows, rb;
-};
-
-template <int NT>
-__device__ __forceinline__ MmItem mm_item(const MatmulArgs &a, long long item, int nrb, const long long *tpre,
-                                          const int *goff) {
-  const long long tile = item / nrb;
-  MmItem m;
-  m.rb = (int)(item - tile * nrb);
-  int lo = 0, hi = a.groups;                               // tpre[lo] <= tile < tpre[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (tpre[mid] <= tile) lo = mid; else hi = mid;
-  }
-  m.g = lo;
-  const int begin = goff[2 * lo], end = goff[2 * lo + 1];
-  m.row0 = begin + (int)(tile - tpre[lo]) * NT;
-  m.nrows = min(NT, end - m.row0);
-  return m;
-}
-
-// The scales of one row for one stage (K elements 256 * it ..): WORDS words.
-// Columns past the row's end read as 1.0 (their codes are zero).
-template <int WORDS>
-__device__ __forceinline__ void load_sf(const uint8_t *row, int it, int nsf, int mode, uint32_t fill, uint32_t (&w)[WORDS]) {
-  const int c0 = it * WORDS * 4;
-  if (mode == 0) {
-    if constexpr (WORDS == 4) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row + c0));
-      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-    } else {
-      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row + c0));
-      w[0] = v.x; w[1] = v.y;
-    }
-  } else if (mode == 1) {
-#pragma unroll
-    for (int i = 0; i < WORDS; ++i)
-      w[i] = c0 + 4 * i < nsf ? __ldg(reinterpret_cast<const uint32_t *>(row + c0 + 4 * i)) : fill;
-  } else {
-#pragma unroll
-    for (int i = 0; i < WORDS; ++i) {
-      w[i] = 0;
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int c = c0 + 4 * i + b;
-        w[i] |= (c < nsf ? (uint32_t)__ldg(row + c) : (fill & 0xFFu)) << (8 * b);
-      }
-    }
-  }
-}
-
-__device__ __forceinline__ void store_out(void *y, int dtype, int64_t at, float v) {
-  if (dtype == MOE_DT_F32) static_cast<float *>(y)[at] = v;
-  else if (dtype == MOE_DT_BF16) static_cast<uint16_t *>(y)[at] = bf16_bits(v);
-  else static_cast<uint16_t *>(y)[at] = f16_bits(v);
-}
-
 template <int WF, int NT, bool SPLIT>
 __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_constant__ MatmulArgs a) {
   using Geo = MmGeom<WF, NT>;
@@ -143,9 +67,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
   __shared__ __align__(8) uint64_t acce_bar[NBUF];
   __shared__ __align__(8) uint64_t quiesce_bar;
   __shared__ uint32_t tmem_base_s;
-  __shared__ long long tpre[kMmMaxGroups + 1];             // tiles before each group
-  __shared__ int goff[2 * kMmMaxGroups];                   // first row and end of each group
-  __shared__ long long wsum[kMmThreads / 32];
+  __shared__ MmGroups groups;
   __shared__ int ok_s;
 
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(mm_raw) + 1023) & ~uintptr_t(1023));
@@ -169,41 +91,13 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
     tmem_relinquish();
   }
   wait_prior_grid();
-  // tiles of each group, scanned: thread t takes `per` consecutive groups
-  {
-    const int per = (a.groups + kMmThreads - 1) / kMmThreads;
-    const int g0 = min(a.groups, tid * per), g1 = min(a.groups, g0 + per);
-    long long sum = 0;
-    for (int g = g0; g < g1; ++g) {
-      const int b = a.offsets ? min(max(__ldg(a.offsets + g), 0), a.rows) : 0;
-      const int e = a.offsets ? min(max(__ldg(a.offsets + g + 1), 0), a.rows) : a.rows;
-      goff[2 * g] = b;
-      goff[2 * g + 1] = max(b, e);
-      tpre[g] = sum;
-      sum += (max(b, e) - b + NT - 1) / NT;
-    }
-    long long inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
-    if (lane == 31) wsum[warp] = inc;
-    __syncthreads();
-    long long earlier = inc - sum, all = 0;
-    for (int w = 0; w < kMmThreads / 32; ++w) {
-      if (w < warp) earlier += wsum[w];
-      all += wsum[w];
-    }
-    for (int g = g0; g < g1; ++g) tpre[g] += earlier;
-    if (tid == 0) tpre[a.groups] = all;
-  }
+  mm_scan_groups<NT>(a, groups);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base_s;
   const int nrb = (a.N + 127) / 128;
-  const long long n_items = tpre[a.groups] * nrb;
+  const long long n_items = (long long)groups.tiles[a.groups] * nrb;
   const int nk_all = (a.K + 255) / 256;
 
   // SPLIT: cluster c takes item c and rank r of it the K range [k0, k1)
@@ -222,7 +116,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
     uint32_t ph = 0;
     bool failed = false;
     for (long long item = first; item < n_items && !failed; item += step) {
-      const MmItem m = mm_item<NT>(a, item, nrb, tpre, goff);
+      const MmItem m = mm_item<NT>(a, groups, item, nrb);
       for (int it = k0; it < k1; ++it) {
         if (issued >= S && !mbar_wait_warp(smem_u32(&empty_bar[s]), ph ^ 1u, a.err, 61)) { failed = true; break; }
         const uint32_t bar = smem_u32(&full_bar[s]);
@@ -301,7 +195,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
       const int quad = warp & 3;
       int n = 0;
       for (long long item = first; item < n_items; item += step) {
-        const MmItem m = mm_item<NT>(a, item, nrb, tpre, goff);
+        const MmItem m = mm_item<NT>(a, groups, item, nrb);
         const int buf = n % NBUF;
         if (!mbar_wait_warp(smem_u32(&accf_bar[buf]), (n / NBUF) & 1, a.err, 64)) break;
         tc_fence_after();
@@ -332,7 +226,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
     // (stage count) % 2 == p.  Row words are loaded one stage of the pair ahead.
     const int pair = (warp - 6) >> 1;
     const bool tokens = (warp & 1) != 0;
-    const uint32_t fill = (WF == WF_MX) ? 0x7F7F7F7Fu : 0x38383838u;
+    const uint32_t fill = kSfOne<WF>;
     constexpr int RG = (NT + 31) / 32 < 4 ? (NT + 31) / 32 : 4;        // 32-row groups of a token tile
     // the (item, stage) sequence this warp loads, and where it stores
     long long item = first;
@@ -341,7 +235,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
     MmItem m{};
     const uint8_t *rowp[4];
     auto rows_of = [&]() {
-      m = mm_item<NT>(a, item, nrb, tpre, goff);
+      m = mm_item<NT>(a, groups, item, nrb);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (tokens) {
@@ -433,7 +327,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
     }
     cluster.sync();                                        // every part is where it is added
     if (any) {
-      const MmItem m = mm_item<NT>(a, first, nrb, tpre, goff);
+      const MmItem m = mm_item<NT>(a, groups, first, nrb);
       const float wG = (WF == WF_NV) ? __ldg(a.wG + m.g) : 1.0f;
       for (int i = tid; i < per * m.nrows; i += kMmThreads) {
         const int c = i / per, r = i - c * per;            // neighbouring threads: neighbouring columns of y
@@ -543,7 +437,8 @@ extern "C" moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_
   static const char fn[] = "moe_fp4_matmul";
   if (fmt != MOE_FMT_MXFP4 && fmt != MOE_FMT_NVFP4) return ops_invalid(fn, "fmt must be MOE_FMT_MXFP4 or MOE_FMT_NVFP4");
   if (!is_float_dtype(dtype)) return ops_invalid(fn, "dtype must be F32, BF16 or F16");
-  if (rows < 0 || N < 1 || K < 32 || K % 32) return ops_invalid(fn, "need rows >= 0, N >= 1 and K a multiple of 32");
+  if (rows < 0 || rows > kMmMaxRows || N < 1 || K < 32 || K % 32)
+    return ops_invalid(fn, "need 0 <= rows <= 2^27, N >= 1 and K a multiple of 32");
   if (n_groups < 1 || n_groups > kMmMaxGroups || (int64_t)n_groups * N >= (int64_t)1 << 31)
     return ops_invalid(fn, "need 1 <= n_groups <= 1024 and n_groups * N below 2^31");
   if (!offsets && n_groups != 1) return ops_invalid(fn, "more than one group needs offsets");
@@ -563,11 +458,15 @@ extern "C" moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_
   // that holds them, so that a decode batch streams weights and little else
   const int64_t mean = (rows + n_groups - 1) / n_groups;
   const int nt = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 128;
+  const int sms = sm_count();
+  // CTA pairs where the rows fill a wide tile and there are items for every pair
+  const int64_t pair_items = (rows / kPairRows + n_groups) * (int64_t)((N + 255) / 256);
+  const bool pairs = mean > 64 && pair_items >= sms / 2;
   const cuuint64_t kb = (cuuint64_t)(K / 2);
   const cuuint32_t ones[3] = {1, 1, 1};
   {
     const cuuint64_t dims[2] = {kb, (cuuint64_t)rows}, strides[1] = {kb};
-    const cuuint32_t box[2] = {128, (cuuint32_t)nt};
+    const cuuint32_t box[2] = {128, (cuuint32_t)(pairs ? kPairBox : nt)};
     if (enc(&a.xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(x_codes), dims, strides, box, ones,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -600,9 +499,14 @@ extern "C" moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_
   a.sf_mode = a.nsf % stage == 0 && aligned_to(x_scales, stage) && aligned_to(w_scales, stage) ? 0
               : a.nsf % 4 == 0 && aligned_to(x_scales, 4) && aligned_to(w_scales, 4)           ? 1
                                                                                               : 2;
+  a.sf_wide = a.sf_mode == 0 && a.nsf % 16 == 0 && aligned_to(x_scales, 16) && aligned_to(w_scales, 16);
+  a.y_vec = row_alignment(y, ldy * dtype_bytes(dtype)) == 16;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (pairs)
+    return ops_launched(fn, launch_matmul_pair(fmt == MOE_FMT_MXFP4 ? WF_MX : WF_NV, a,
+                                               (int)std::min<int64_t>(pair_items, sms / 2), s));
   // items there can be at most, and the ways to split K when they leave SMs idle:
   // each way keeps at least two stages
-  const int sms = sm_count();
   const int64_t nrb = (N + 127) / 128;
   const int64_t tiles = std::min<int64_t>(rows, rows / nt + n_groups);
   const int64_t items = tiles * nrb;
@@ -610,7 +514,6 @@ extern "C" moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_
   int ranks = 1;
   while (ranks < 8 && items * ranks * 2 <= sms && nk >= 4 * ranks) ranks *= 2;
   const int grid = (int)std::min<int64_t>(items, ranks > 1 ? items : sms);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = fmt == MOE_FMT_MXFP4 ? run_matmul<WF_MX>(a, nt, grid, ranks, s)
                                              : run_matmul<WF_NV>(a, nt, grid, ranks, s);
   return ops_launched(fn, e);

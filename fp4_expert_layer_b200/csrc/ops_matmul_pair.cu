@@ -1,0 +1,395 @@
+// ops_matmul_pair.cu -- the grouped FP4 product for many rows: CTA pairs.
+//
+//   y[r, n] = xG[r] wG[g] sum_k x[r, k] w[g, n, k]
+//
+// Two CTAs of a cluster share one MMA of 256 weight rows x up to 256 token rows
+// (cta_group::2): each holds 128 weight rows and half the tokens' rows, so that a
+// stage of 256 K elements brings 32 KB of codes to an SM for 128 x 256 x 256
+// multiply-adds.  One CTA's 128 x 128 tile brings the same for half of them, and
+// what bounds the product is this fill, L2 to shared memory (about 45 bytes a
+// clock an SM reach it), not the tensor pipe.
+//
+// The MMA is as wide as the item has rows (rounded up to 32), and boxes of 64 rows
+// that it does not need are not copied, so a ragged segment costs what it holds.
+//
+// TMEM: two accumulators of 256 columns overlap: [0, 256) and [B1, B1 + 256), with
+// B1 as far up as two stages' scales leave room.  An item's epilogue reads the
+// shared columns first and hands them on, then reads the rest while the next item
+// multiplies.  tcgen05.cp and MMAs of one thread run in order, so scales need no
+// more than two places.
+//
+// Warps of each CTA: 0 copies codes; 1 allocates TMEM and, in the even CTA, issues
+// for both; 2..9 read accumulators back (two a lane quadrant, on alternate 32-token
+// chunks); 10 brings the scales of the weights, 11 and 12 those of the tokens' two
+// halves: 32 bytes of a row at a time (a whole sector: two stages' NVFP4 scales,
+// four stages' MXFP4 ones), one such step ahead, turned over into the blocks that
+// tcgen05.cp copies.
+#include "ops_matmul.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace moe {
+namespace {
+
+constexpr int kPairThreads = 13 * 32;
+constexpr int kPairEpi = 8;                                // epilogue warps of a CTA
+
+template <int WF>
+struct PairGeom {
+  static constexpr int NBLK = (WF == WF_MX) ? 2 : 4;       // 4-scale blocks of 256 K
+  static constexpr int WORDS = NBLK;                       // words of scales a row has in a stage
+  static constexpr int AHEAD = 8 / WORDS;                  // stages that 32 bytes of a row's scales are
+  static constexpr int A_BYTES = 128 * 128;
+  static constexpr int BOX_BYTES = kPairBox * 128;
+  static constexpr int SFA_OFF = 2 * A_BYTES;              // codes: 128 weight rows, then 128 token rows
+  static constexpr int SFB_OFF = SFA_OFF + NBLK * 512;
+  static constexpr int STAGE = SFB_OFF + NBLK * 1024;      // 35 KB (MXFP4), 38 KB (NVFP4)
+  static constexpr int STAGES = 5;
+  static constexpr int SF_COLS = 12 * NBLK;                // TMEM columns of a stage's scales
+  static constexpr int SF_TMEM = 512 - 2 * SF_COLS;
+  static constexpr int B1 = SF_TMEM - 256;                 // where the second accumulator starts
+  static constexpr int TURN = 32 * 80;                     // an epilogue warp's turning space
+  static constexpr size_t SMEM = (size_t)STAGES * STAGE + kPairEpi * TURN + 1024;
+  static_assert(STAGE % 1024 == 0, "stages keep the 1024-byte swizzle alignment");
+  static_assert(SMEM + 13 * 1024 <= 227 * 1024, "shared-memory budget");
+};
+
+template <int WF>
+__global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const __grid_constant__ MatmulArgs a) {
+  using Geo = PairGeom<WF>;
+  constexpr int S = Geo::STAGES, WORDS = Geo::WORDS, NBLK = Geo::NBLK;
+  extern __shared__ __align__(1024) uint8_t pm_raw[];
+  __shared__ __align__(8) uint64_t full_bar[S];            // the even CTA's: both CTAs' copies and scales
+  __shared__ __align__(8) uint64_t empty_bar[S];           // each CTA's: the MMAs of the stage are done
+  __shared__ __align__(8) uint64_t accf_bar[2];            // each CTA's: an accumulator is complete
+  __shared__ __align__(8) uint64_t free_bar;               // the even CTA's: the shared columns are read
+  __shared__ __align__(8) uint64_t quiesce_bar;
+  __shared__ uint32_t tmem_base_s;
+  __shared__ MmGroups groups;
+
+  cg::cluster_group cluster = cg::this_cluster();
+  const uint32_t rank = cluster.block_rank();
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(pm_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&full_bar[s]), 1 + 2 * 3);        // the copies' bytes, three scale warps of each CTA
+      mbar_init(smem_u32(&empty_bar[s]), 1);
+    }
+    mbar_init(smem_u32(&accf_bar[0]), 1);
+    mbar_init(smem_u32(&accf_bar[1]), 1);
+    mbar_init(smem_u32(&free_bar), 2 * kPairEpi);
+    mbar_init(smem_u32(&quiesce_bar), 1);
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(&tmem_base_s), 512);
+    tmem_relinquish_pair();
+  }
+  wait_prior_grid();
+  mm_scan_groups<kPairRows>(a, groups);
+  tc_fence_before();
+  __syncthreads();
+  cluster.sync();                                          // both CTAs' barriers and TMEM are ready
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_s;
+  const int nrb = (a.N + 255) / 256;
+  const long long n_items = (long long)groups.tiles[a.groups] * nrb;
+  const int nk = (a.K + 255) / 256;
+  const long long first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+  if (warp == 0) {
+    // ---------------- codes of this CTA's rows; their bytes count on the even CTA's barrier
+    int s = 0, issued = 0;
+    uint32_t ph = 0;
+    bool failed = false;
+    for (long long item = first; item < n_items && !failed; item += step) {
+      const MmItem m = mm_item<kPairRows>(a, groups, item, nrb);
+      const int half = (m.nrows + 31) / 32 * 16;           // token rows of each CTA
+      const int boxes = (half + kPairBox - 1) / kPairBox;
+      const int wrow = m.rb * 256 + (int)rank * 128, xrow = m.row0 + (int)rank * half;
+      for (int it = 0; it < nk; ++it) {
+        if (issued >= S && !mbar_wait_warp(smem_u32(&empty_bar[s]), ph ^ 1u, a.err, 71)) { failed = true; break; }
+        const uint32_t bar = cluster_addr(smem_u32(&full_bar[s]), 0);
+        const uint32_t st = smem_u32(smem + (size_t)s * Geo::STAGE);
+        if (elect_one()) {
+          if (rank == 0)
+            mbar_arrive_expect_tx(smem_u32(&full_bar[s]), (uint32_t)(2 * (Geo::A_BYTES + boxes * Geo::BOX_BYTES)));
+          tma_load_3d_pair(st, &a.wmap, bar, it * 128, wrow, m.g);
+          for (int b = 0; b < boxes; ++b)
+            tma_load_2d_pair(st + Geo::A_BYTES + b * Geo::BOX_BYTES, &a.xmap, bar, it * 128, xrow + b * kPairBox);
+        }
+        __syncwarp();
+        ++issued;
+        if (++s == S) { s = 0; ph ^= 1u; }
+      }
+    }
+    // every copy of the pair has landed before it leaves (the other CTA waits at
+    // the cluster's last barrier)
+    if (rank == 0 && lane == 0) {
+      int s2 = 0;
+      uint32_t ph2 = 0;
+      for (int i = 0; i < issued; ++i) {
+        if (i >= issued - S) mbar_drain(smem_u32(&full_bar[s2]), ph2);
+        if (++s2 == S) { s2 = 0; ph2 ^= 1u; }
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------- MMAs of the pair, issued by the even CTA
+    if (rank == 0) {
+      int s = 0, n = 0, turn = 0;
+      uint32_t ph = 0;
+      bool failed = false;
+      for (long long item = first; item < n_items && !failed; item += step) {
+        const MmItem m = mm_item<kPairRows>(a, groups, item, nrb);
+        const int cols = __shfl_sync(0xffffffffu, (m.nrows + 31) / 32 * 32, 0);
+        const uint32_t acc = tmem + ((n & 1) ? (uint32_t)Geo::B1 : 0u);
+        const uint32_t id0 = idesc_fp4_block(256, cols, WF == WF_MX, 0, 0);
+        const uint32_t id2 = idesc_fp4_block(256, cols, WF == WF_MX, 2, 2);
+        if (n > 0 && !mbar_wait_warp(smem_u32(&free_bar), (n - 1) & 1, a.err, 72)) break;
+        tc_fence_after();
+        for (int it = 0; it < nk; ++it) {
+          if (!mbar_wait_warp(smem_u32(&full_bar[s]), ph, a.err, 73)) { failed = true; break; }
+          tc_fence_after();
+          const uint32_t st = smem_u32(smem + (size_t)s * Geo::STAGE);
+          const uint32_t sf = tmem + (uint32_t)(Geo::SF_TMEM + turn * Geo::SF_COLS);
+          if (elect_one()) {
+#pragma unroll
+            for (int b = 0; b < NBLK; ++b) {
+              tc_cp_sf_block_pair(sf + 4 * b, st + Geo::SFA_OFF + 512 * b);
+              tc_cp_sf_block_pair(sf + 4 * NBLK + 8 * b, st + Geo::SFB_OFF + 1024 * b);
+              if (cols > 128) tc_cp_sf_block_pair(sf + 4 * NBLK + 8 * b + 4, st + Geo::SFB_OFF + 1024 * b + 512);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {                  // K = 64 an MMA
+              const int blk = (WF == WF_MX) ? (k >> 1) : k;
+              const uint32_t byte = (WF == WF_MX) ? (uint32_t)(2 * (k & 1)) : 0u;
+              const uint64_t adesc = umma_desc(st + k * 32, 16, 1024, 2);
+              const uint64_t bdesc = umma_desc(st + Geo::A_BYTES + k * 32, 16, 1024, 2);
+              const uint32_t sfa = (sf + (uint32_t)(4 * blk)) | (byte << 30);
+              const uint32_t sfb = (sf + (uint32_t)(4 * NBLK + 8 * blk)) | (byte << 30);
+              const uint32_t accum = (it > 0 || k > 0) ? 1u : 0u;
+              if constexpr (WF == WF_MX) umma_mxf4_pair(acc, adesc, bdesc, byte ? id2 : id0, sfa, sfb, accum);
+              else umma_nvf4_pair(acc, adesc, bdesc, id0, sfa, sfb, accum);
+            }
+            tc_commit_pair(smem_u32(&empty_bar[s]), 3);
+          }
+          __syncwarp();
+          turn ^= 1;
+          if (++s == S) { s = 0; ph ^= 1u; }
+        }
+        if (failed) break;
+        if (elect_one()) tc_commit_pair(smem_u32(&accf_bar[n & 1]), 3);
+        __syncwarp();
+        ++n;
+      }
+      __syncwarp();
+      if (elect_one()) tc_commit_pair(smem_u32(&quiesce_bar), 1);   // all done, also after a wait gave up
+      __syncwarp();
+      mbar_drain(smem_u32(&quiesce_bar), 0);
+    }
+  } else if (warp < 2 + kPairEpi) {
+    // ---------------- accumulators to y: TMEM lanes 32 * (w % 4) .. are weight rows,
+    // columns are token rows
+    const int quad = warp & 3, odd = (warp - 2) >> 2;
+    uint8_t *turn = smem + (size_t)S * Geo::STAGE + (warp - 2) * Geo::TURN;
+    const uint32_t free_even = cluster_addr(smem_u32(&free_bar), 0);
+    const int es = a.dtype == MOE_DT_F32 ? 4 : 2;
+    int n = 0;
+    for (long long item = first; item < n_items; item += step) {
+      const MmItem m = mm_item<kPairRows>(a, groups, item, nrb);
+      const int buf = n & 1;
+      if (!mbar_wait_warp(smem_u32(&accf_bar[buf]), (n >> 1) & 1, a.err, 74)) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + (buf ? (uint32_t)Geo::B1 : 0u) + ((uint32_t)(32 * quad) << 16);
+      const int chunks = (m.nrows + 31) / 32;
+      const int col0 = m.rb * 256 + (int)rank * 128 + 32 * quad, col = col0 + lane;
+      const float wG = (WF == WF_NV) ? __ldg(a.wG + m.g) : 1.0f;
+      const bool rows16 = es == 2 && a.y_vec && col0 + 32 <= a.N;
+      // the first accumulator shares its last columns, the second its first ones:
+      // those chunks go first
+      int shared_left = 0;
+      for (int i = odd; i < chunks; i += 2) {
+        const int c = buf ? i : chunks - 1 - i;
+        if (buf ? 32 * c < 256 - Geo::B1 : 32 * c + 32 > Geo::B1) ++shared_left;
+      }
+      if (shared_left == 0) {
+        if (lane == 0) mbar_arrive_cluster(free_even);
+        shared_left = -1;
+      }
+      for (int i = odd; i < chunks; i += 2) {
+        const int c = buf ? i : chunks - 1 - i;
+        uint32_t d[32];
+        tmem_ld32(acc + (uint32_t)(32 * c), d);
+        const int have = min(32, m.nrows - 32 * c);
+        const float xG = (WF == WF_NV && lane < have) ? wG * __ldg(a.xG + m.row0 + 32 * c + lane) : 1.0f;
+        tmem_ld_wait();
+        if (--shared_left == 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(free_even);
+        }
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          v[j] = (WF == WF_NV) ? __uint_as_float(d[j]) * __shfl_sync(0xffffffffu, xG, j) : __uint_as_float(d[j]);
+        const int64_t at = (int64_t)(m.row0 + 32 * c) * a.ldy;
+        if (rows16) {
+          // 16-bit rows: turned over in shared memory to 64 bytes of a token's row
+          uint16_t *mine = reinterpret_cast<uint16_t *>(turn) + lane;
+          if (a.dtype == MOE_DT_BF16) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) mine[40 * j] = bf16_bits(v[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) mine[40 * j] = f16_bits(v[j]);
+          }
+          __syncwarp();
+          uint16_t *y = static_cast<uint16_t *>(a.y) + at + col0 + 8 * (lane & 3);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int r = 8 * q + (lane >> 2);
+            const uint4 w = *reinterpret_cast<const uint4 *>(turn + 80 * r + 16 * (lane & 3));
+            if (r < have) *reinterpret_cast<uint4 *>(y + (int64_t)r * a.ldy) = w;
+          }
+          __syncwarp();
+        } else if (col < a.N) {
+          if (a.dtype == MOE_DT_F32) {
+            float *y = static_cast<float *>(a.y) + at + col;
+#pragma unroll
+            for (int j = 0; j < 32; ++j, y += a.ldy)
+              if (j < have) *y = v[j];
+          } else {
+            uint16_t *y = static_cast<uint16_t *>(a.y) + at + col;
+#pragma unroll
+            for (int j = 0; j < 32; ++j, y += a.ldy)
+              if (j < have) *y = a.dtype == MOE_DT_BF16 ? bf16_bits(v[j]) : f16_bits(v[j]);
+          }
+        }
+      }
+      ++n;
+    }
+  } else {
+    // ---------------- scales: `which` 0 the weights', 1 and 2 the tokens' halves
+    const int which = warp - (2 + kPairEpi);
+    const int off = which == 0 ? Geo::SFA_OFF : Geo::SFB_OFF + 512 * (which - 1);
+    const int pitch = which == 0 ? 512 : 1024;             // between a stage's blocks
+    const uint32_t fill = kSfOne<WF>;
+    const uint8_t *rowp[4];
+    uint32_t cur[4][8];
+    bool wanted = false;                                   // the second half of a narrow tile is not read
+    auto rows_of = [&](long long item) {
+      const MmItem m = mm_item<kPairRows>(a, groups, item, nrb);
+      wanted = which < 2 || m.nrows > 128;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (which == 0) {
+          const int r = min(m.rb * 256 + (int)rank * 128 + 32 * j + lane, a.N - 1);
+          rowp[j] = a.ws + ((size_t)m.g * a.N + r) * a.nsf;
+        } else {
+          const int r = min(m.row0 + 128 * (which - 1) + 32 * j + lane, a.rows - 1);
+          rowp[j] = a.xs + (size_t)r * a.nsf;
+        }
+      }
+    };
+    auto fetch = [&](int it0) {                            // 32 bytes of each row, from stage it0 on
+      if (!wanted) return;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (a.sf_wide && it0 + Geo::AHEAD <= nk) {
+          const uint4 *p = reinterpret_cast<const uint4 *>(rowp[j] + it0 * 4 * WORDS);
+          const uint4 lo = __ldg(p), hi = __ldg(p + 1);
+          cur[j][0] = lo.x; cur[j][1] = lo.y; cur[j][2] = lo.z; cur[j][3] = lo.w;
+          cur[j][4] = hi.x; cur[j][5] = hi.y; cur[j][6] = hi.z; cur[j][7] = hi.w;
+          continue;
+        }
+#pragma unroll
+        for (int i = 0; i < Geo::AHEAD; ++i)
+          if (it0 + i < nk) load_sf<WORDS>(rowp[j], it0 + i, a.nsf, a.sf_mode, fill, &cur[j][i * WORDS]);
+      }
+    };
+    long long item = first;
+    int it0 = 0, s = 0, issued = 0;
+    uint32_t ph = 0;
+    bool more = item < n_items;
+    if (more) {
+      rows_of(item);
+      fetch(0);
+    }
+    bool failed = false;
+    while (more && !failed) {
+      uint32_t hold[4][8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) hold[j][i] = cur[j][i];
+      const int stages = min(Geo::AHEAD, nk - it0);
+      const bool put = wanted;
+      it0 += Geo::AHEAD;
+      if (it0 >= nk) {
+        it0 = 0;
+        item += step;
+        more = item < n_items;
+        if (more) rows_of(item);
+      }
+      if (more) fetch(it0);
+#pragma unroll
+      for (int i = 0; i < Geo::AHEAD; ++i) {
+        if (i >= stages || failed) break;
+        if (issued >= S && !mbar_wait_warp(smem_u32(&empty_bar[s]), ph ^ 1u, a.err, 75)) { failed = true; break; }
+        if (put) {
+          const uint32_t dst = smem_u32(smem + (size_t)s * Geo::STAGE) + off + 16 * lane;
+#pragma unroll
+          for (int b = 0; b < WORDS; ++b)
+            sts128(dst + pitch * b, make_uint4(hold[0][i * WORDS + b], hold[1][i * WORDS + b], hold[2][i * WORDS + b],
+                                               hold[3][i * WORDS + b]));
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&full_bar[s]), 0));
+        ++issued;
+        if (++s == S) { s = 0; ph ^= 1u; }
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  cluster.sync();                                          // no CTA leaves, or frees TMEM, while the other works
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <int WF>
+cudaError_t launch_pair(const MatmulArgs &a, int pairs, cudaStream_t s) {
+  using Geo = PairGeom<WF>;
+  auto fn = fp4_matmul_pair_kernel<WF>;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Geo::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * pairs));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = Geo::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, fn, a);
+}
+
+}  // namespace
+
+cudaError_t launch_matmul_pair(int wf, const MatmulArgs &a, int pairs, cudaStream_t s) {
+  return wf == WF_MX ? launch_pair<WF_MX>(a, pairs, s) : launch_pair<WF_NV>(a, pairs, s);
+}
+
+}  // namespace moe

@@ -75,7 +75,7 @@ moe_status_t moe_fp4_dequantize(const uint8_t *codes, const uint8_t *scales, con
  * or behind offsets[n_groups] are left as they were.  Sums do not depend on the
  * order in which the GPU runs them: equal calls give equal bits.
  * K is a multiple of 32, 1 <= n_groups <= 1024; codes are 16-byte aligned and y
- * aligned to its type; rows, N, K and n_groups * N below 2^31.  The scale rows
+ * aligned to its type; rows <= 2^27; N, K and n_groups * N below 2^31.  The scale rows
  * are read fastest when K is a multiple of 256 and they are 16-byte aligned. */
 moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_scales, const float *x_global, int32_t rows,
                             const uint8_t *w_codes, const uint8_t *w_scales, const float *w_global, int32_t n_groups,

@@ -412,6 +412,29 @@ def test_grouped_product(fmt, lens, behind, N, K):
         assert t.equal(y, again)
 
 
+WIDE = [  # many rows: segment lengths, rows behind, N, K
+    ([1300], 0, 4000, 288), ([2561], 3, 2100, 1024), ([700, 0, 257, 256, 1, 95, 300], 5, 3328, 1056),
+    ([90, 33, 161, 128, 129, 255] * 6, 0, 513, 2048), ([150, 20, 400, 60] * 5, 2, 1280, 4096),
+]
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("lens, behind, N, K", WIDE)
+def test_product_of_many_rows(fmt, lens, behind, N, K):
+    t, F = G.torch(), G.library()
+    rows, E = sum(lens) + behind, len(lens)
+    x, w = _operands(fmt, rows, E, N, K, rows + N + K)
+    off = t.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=t.int32, device="cuda")
+    for out, pad, shift in (("f32", 0, 0), ("bf16", 0, 0), ("bf16", 3, 1), ("bf16", 8, 8)):
+        y0 = placed(randn((rows, N), 1, out), pad, shift)
+        y = placed(y0, pad, shift)
+        F.fp4_matmul(x, w, off, out=y)
+        _check_product(x, w, off, y0, y, out)
+        again = placed(y0, pad, shift)
+        F.fp4_matmul(x, w, off, out=again)
+        assert t.equal(y, again)
+
+
 def test_grouped_product_of_a_first_row_past_zero():
     """offsets[0] > 0: the rows before the first segment stay as they are too."""
     t, F = G.torch(), G.library()
@@ -440,7 +463,7 @@ def test_offsets_out_of_range_are_cut_to_the_rows():
 @pytest.mark.parametrize("shift", [0, 1, 4])
 def test_product_of_scales_that_are_not_aligned(fmt, shift):
     t, F = G.torch(), G.library()
-    for rows, N, K in ((20, 130, 512), (5, 64, 128)):
+    for rows, N, K in ((20, 130, 512), (5, 64, 128), (1200, 3900, 256)):
         x, w = _operands(fmt, rows, 1, N, K, 5)
 
         def moved(s):
