@@ -97,7 +97,6 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
   tc_fence_after();
   const uint32_t tmem = tmem_base_s;
   const int nrb = (a.N + 127) / 128;
-  const long long n_items = (long long)groups.tiles[a.groups] * nrb;
   const int nk_all = (a.K + 255) / 256;
 
   // SPLIT: cluster c takes item c and rank r of it the K range [k0, k1)
@@ -108,15 +107,15 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
   }
   const int k0 = nk_all * rank / ranks, k1 = nk_all * (rank + 1) / ranks;
   const long long first = SPLIT ? blockIdx.x / ranks : blockIdx.x;
-  const long long step = SPLIT ? n_items + 1 : gridDim.x;  // one item at most when split
+  const long long step = SPLIT ? (long long)(groups.tiles[a.groups] + 1) * nrb : gridDim.x;   // split: one item at most
+  using Walk = MmWalk<NT>;
 
   if (warp == 0) {
     // ---------------- codes
     int s = 0, issued = 0;
     uint32_t ph = 0;
     bool failed = false;
-    for (long long item = first; item < n_items && !failed; item += step) {
-      const MmItem m = mm_item<NT>(a, groups, item, nrb);
+    for (Walk m(a, groups, nrb, first, step); m.more() && !failed; m.next(a, groups)) {
       for (int it = k0; it < k1; ++it) {
         if (issued >= S && !mbar_wait_warp(smem_u32(&empty_bar[s]), ph ^ 1u, a.err, 61)) { failed = true; break; }
         const uint32_t bar = smem_u32(&full_bar[s]);
@@ -146,7 +145,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
     int s = 0, n = 0;
     uint32_t ph = 0;
     bool failed = false;
-    for (long long item = first; item < n_items && !failed; item += step) {
+    for (Walk m(a, groups, nrb, first, step); m.more() && !failed; m.next(a, groups)) {
       const int buf = n % NBUF;
       if (n >= NBUF && !mbar_wait_warp(smem_u32(&acce_bar[buf]), ((n / NBUF) - 1) & 1, a.err, 62)) break;
       tc_fence_after();
@@ -194,8 +193,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
     if constexpr (!SPLIT) {
       const int quad = warp & 3;
       int n = 0;
-      for (long long item = first; item < n_items; item += step) {
-        const MmItem m = mm_item<NT>(a, groups, item, nrb);
+      for (Walk m(a, groups, nrb, first, step); m.more(); m.next(a, groups)) {
         const int buf = n % NBUF;
         if (!mbar_wait_warp(smem_u32(&accf_bar[buf]), (n / NBUF) & 1, a.err, 64)) break;
         tc_fence_after();
@@ -229,13 +227,11 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
     const uint32_t fill = kSfOne<WF>;
     constexpr int RG = (NT + 31) / 32 < 4 ? (NT + 31) / 32 : 4;        // 32-row groups of a token tile
     // the (item, stage) sequence this warp loads, and where it stores
-    long long item = first;
+    Walk m(a, groups, nrb, first, step);
     int it = k0, seq = 0;
-    bool have = item < n_items && k1 > k0;
-    MmItem m{};
+    bool have = m.more() && k1 > k0;
     const uint8_t *rowp[4];
     auto rows_of = [&]() {
-      m = mm_item<NT>(a, groups, item, nrb);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (tokens) {
@@ -252,8 +248,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
       ++seq;
       if (++it == k1) {
         it = k0;
-        item += step;
-        have = item < n_items;
+        m.next(a, groups);
+        have = m.more();
         if (have) rows_of();
       }
     };
@@ -299,7 +295,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
     // parts meet: rank q finishes weight rows [128 q / ranks, 128 (q + 1) / ranks)
     cg::cluster_group cluster = cg::this_cluster();
     float *recv = reinterpret_cast<float *>(smem);         // [source][rows of a rank][NT], over the stages
-    const bool any = first < n_items;                      // the same for the whole cluster
+    const Walk m(a, groups, nrb, first, step);
+    const bool any = m.more();                             // the same for the whole cluster
     if (any && warp >= 2 && warp < 6) {
       if (!mbar_wait_warp(smem_u32(&accf_bar[0]), 0, a.err, 66) && lane == 0) ok_s = 0;
     }
@@ -327,7 +324,6 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
     }
     cluster.sync();                                        // every part is where it is added
     if (any) {
-      const MmItem m = mm_item<NT>(a, groups, first, nrb);
       const float wG = (WF == WF_NV) ? __ldg(a.wG + m.g) : 1.0f;
       for (int i = tid; i < per * m.nrows; i += kMmThreads) {
         const int c = i / per, r = i - c * per;            // neighbouring threads: neighbouring columns of y

@@ -70,25 +70,44 @@ __device__ __forceinline__ void mm_scan_groups(const MatmulArgs &a, MmGroups &t)
   if (tid == 0) t.tiles[a.groups] = all;
 }
 
-struct MmItem {
-  int g, row0, nrows, rb;        // group, first row, rows, block of weight rows
-};
-
+// A warp's walk over the items first, first + step, ...: item = tile * nrb + row
+// block, the tiles in group order.  Whole warps walk (the groups are searched 32
+// at a time); values are warp-uniform.
 template <int NT>
-__device__ __forceinline__ MmItem mm_item(const MatmulArgs &a, const MmGroups &t, long long item, int nrb) {
-  const int tile = (int)(item / nrb);
-  MmItem m;
-  m.rb = (int)(item - (long long)tile * nrb);
-  int lo = 0, hi = a.groups;     // tiles[lo] <= tile < tiles[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (t.tiles[mid] <= tile) lo = mid; else hi = mid;
+struct MmWalk {
+  int g, row0, nrows, rb;        // of the item: group, first row, rows, block of weight rows
+  int tile, dtile, drb, nrb, ntiles;
+  __device__ __forceinline__ MmWalk(const MatmulArgs &a, const MmGroups &t, int nrb_, long long first, long long step)
+      : g(0), nrb(nrb_), ntiles(t.tiles[a.groups]) {
+    tile = (int)(first / nrb);
+    rb = (int)(first - (long long)tile * nrb);
+    dtile = (int)(step / nrb);
+    drb = (int)(step - (long long)dtile * nrb);
+    find(a, t);
   }
-  m.g = lo;
-  m.row0 = t.begin[lo] + (tile - t.tiles[lo]) * NT;
-  m.nrows = min(NT, t.end[lo] - m.row0);
-  return m;
-}
+  __device__ __forceinline__ bool more() const { return tile < ntiles; }
+  __device__ __forceinline__ void next(const MatmulArgs &a, const MmGroups &t) {
+    tile += dtile;
+    rb += drb;
+    if (rb >= nrb) {
+      rb -= nrb;
+      ++tile;
+    }
+    find(a, t);
+  }
+  __device__ __forceinline__ void find(const MatmulArgs &a, const MmGroups &t) {
+    if (!more()) return;
+    const int lane = threadIdx.x & 31;
+    while (true) {               // the last group that starts at or before the tile
+      const int c = g + 1 + lane;
+      const unsigned passed = __ballot_sync(0xffffffffu, c < a.groups && t.tiles[c] <= tile);
+      g += __popc(passed);
+      if (passed != 0xffffffffu) break;
+    }
+    row0 = t.begin[g] + (tile - t.tiles[g]) * NT;
+    nrows = min(NT, t.end[g] - row0);
+  }
+};
 
 // ---------------------------------------------------------------------- scales
 // The scales of one row for one stage (K elements 256 * it ..): WORDS words.

@@ -12,11 +12,11 @@
 // The MMA is as wide as the item has rows (rounded up to 32), and boxes of 64 rows
 // that it does not need are not copied, so a ragged segment costs what it holds.
 //
-// TMEM: two accumulators of 256 columns overlap: [0, 256) and [B1, B1 + 256), with
-// B1 as far up as two stages' scales leave room.  An item's epilogue reads the
-// shared columns first and hands them on, then reads the rest while the next item
-// multiplies.  tcgen05.cp and MMAs of one thread run in order, so scales need no
-// more than two places.
+// TMEM: items put their accumulators in turn at the lower and the upper end of the
+// columns that two stages' scales leave (416 or 464), where wide ones overlap in
+// the middle.  An epilogue reads the middle first and hands it on, then stores
+// while the next item multiplies.  tcgen05.cp and MMAs of one thread run in order,
+// so scales need no more than two places.
 //
 // Warps of each CTA: 0 copies codes; 1 allocates TMEM and, in the even CTA, issues
 // for both; 2..9 read accumulators back (two a lane quadrant, on alternate 32-token
@@ -47,7 +47,6 @@ struct PairGeom {
   static constexpr int STAGES = 5;
   static constexpr int SF_COLS = 12 * NBLK;                // TMEM columns of a stage's scales
   static constexpr int SF_TMEM = 512 - 2 * SF_COLS;
-  static constexpr int B1 = SF_TMEM - 256;                 // where the second accumulator starts
   static constexpr int TURN = 32 * 80;                     // an epilogue warp's turning space
   static constexpr size_t SMEM = (size_t)STAGES * STAGE + kPairEpi * TURN + 1024;
   static_assert(STAGE % 1024 == 0, "stages keep the 1024-byte swizzle alignment");
@@ -95,17 +94,16 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
   tc_fence_after();
   const uint32_t tmem = tmem_base_s;
   const int nrb = (a.N + 255) / 256;
-  const long long n_items = (long long)groups.tiles[a.groups] * nrb;
   const int nk = (a.K + 255) / 256;
   const long long first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  using Walk = MmWalk<kPairRows>;
 
   if (warp == 0) {
     // ---------------- codes of this CTA's rows; their bytes count on the even CTA's barrier
     int s = 0, issued = 0;
     uint32_t ph = 0;
     bool failed = false;
-    for (long long item = first; item < n_items && !failed; item += step) {
-      const MmItem m = mm_item<kPairRows>(a, groups, item, nrb);
+    for (Walk m(a, groups, nrb, first, step); m.more() && !failed; m.next(a, groups)) {
       const int half = (m.nrows + 31) / 32 * 16;           // token rows of each CTA
       const int boxes = (half + kPairBox - 1) / kPairBox;
       const int wrow = m.rb * 256 + (int)rank * 128, xrow = m.row0 + (int)rank * half;
@@ -141,10 +139,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
       int s = 0, n = 0, turn = 0;
       uint32_t ph = 0;
       bool failed = false;
-      for (long long item = first; item < n_items && !failed; item += step) {
-        const MmItem m = mm_item<kPairRows>(a, groups, item, nrb);
+      Walk m(a, groups, nrb, first, step);
+      while (m.more() && !failed) {
         const int cols = __shfl_sync(0xffffffffu, (m.nrows + 31) / 32 * 32, 0);
-        const uint32_t acc = tmem + ((n & 1) ? (uint32_t)Geo::B1 : 0u);
+        const uint32_t acc = tmem + ((n & 1) ? (uint32_t)(Geo::SF_TMEM - cols) : 0u);
+        m.next(a, groups);                                 // ahead of the waits
         const uint32_t id0 = idesc_fp4_block(256, cols, WF == WF_MX, 0, 0);
         const uint32_t id2 = idesc_fp4_block(256, cols, WF == WF_MX, 2, 2);
         if (n > 0 && !mbar_wait_warp(smem_u32(&free_bar), (n - 1) & 1, a.err, 72)) break;
@@ -197,43 +196,33 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
     const uint32_t free_even = cluster_addr(smem_u32(&free_bar), 0);
     const int es = a.dtype == MOE_DT_F32 ? 4 : 2;
     int n = 0;
-    for (long long item = first; item < n_items; item += step) {
-      const MmItem m = mm_item<kPairRows>(a, groups, item, nrb);
+    for (Walk m(a, groups, nrb, first, step); m.more(); m.next(a, groups), ++n) {
       const int buf = n & 1;
-      if (!mbar_wait_warp(smem_u32(&accf_bar[buf]), (n >> 1) & 1, a.err, 74)) break;
-      tc_fence_after();
-      const uint32_t acc = tmem + (buf ? (uint32_t)Geo::B1 : 0u) + ((uint32_t)(32 * quad) << 16);
       const int chunks = (m.nrows + 31) / 32;
       const int col0 = m.rb * 256 + (int)rank * 128 + 32 * quad, col = col0 + lane;
-      const float wG = (WF == WF_NV) ? __ldg(a.wG + m.g) : 1.0f;
       const bool rows16 = es == 2 && a.y_vec && col0 + 32 <= a.N;
-      // the first accumulator shares its last columns, the second its first ones:
-      // those chunks go first
-      int shared_left = 0;
-      for (int i = odd; i < chunks; i += 2) {
-        const int c = buf ? i : chunks - 1 - i;
-        if (buf ? 32 * c < 256 - Geo::B1 : 32 * c + 32 > Geo::B1) ++shared_left;
-      }
-      if (shared_left == 0) {
-        if (lane == 0) mbar_arrive_cluster(free_even);
-        shared_left = -1;
-      }
-      for (int i = odd; i < chunks; i += 2) {
-        const int c = buf ? i : chunks - 1 - i;
-        uint32_t d[32];
-        tmem_ld32(acc + (uint32_t)(32 * c), d);
-        const int have = min(32, m.nrows - 32 * c);
-        const float xG = (WF == WF_NV && lane < have) ? wG * __ldg(a.xG + m.row0 + 32 * c + lane) : 1.0f;
-        tmem_ld_wait();
-        if (--shared_left == 0) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(free_even);
+      // the chunk of a turn: the first accumulator shares its last columns with the
+      // second, which shares its first ones, so those chunks go first
+      auto chunk = [&](int i) { return buf ? i : chunks - 1 - i; };
+      float xG[4];                                         // this warp's chunks' row scales times the matrix's
+      if constexpr (WF == WF_NV) {
+        const float wG = __ldg(a.wG + m.g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 32 * chunk(2 * i + odd) + lane;
+          xG[i] = 2 * i + odd < chunks && r < m.nrows ? wG * __ldg(a.xG + m.row0 + r) : 1.0f;
         }
+      }
+      if (!mbar_wait_warp(smem_u32(&accf_bar[buf]), (n >> 1) & 1, a.err, 74)) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + (buf ? (uint32_t)(Geo::SF_TMEM - 32 * chunks) : 0u) + ((uint32_t)(32 * quad) << 16);
+
+      auto store = [&](const uint32_t (&d)[32], int c, float g) {
+        const int have = min(32, m.nrows - 32 * c);
         float v[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-          v[j] = (WF == WF_NV) ? __uint_as_float(d[j]) * __shfl_sync(0xffffffffu, xG, j) : __uint_as_float(d[j]);
+          v[j] = (WF == WF_NV) ? __uint_as_float(d[j]) * __shfl_sync(0xffffffffu, g, j) : __uint_as_float(d[j]);
         const int64_t at = (int64_t)(m.row0 + 32 * c) * a.ldy;
         if (rows16) {
           // 16-bit rows: turned over in shared memory to 64 bytes of a token's row
@@ -267,8 +256,24 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
               if (j < have) *y = a.dtype == MOE_DT_BF16 ? bf16_bits(v[j]) : f16_bits(v[j]);
           }
         }
+      };
+      // a warp has at most two chunks with shared columns: once its first two turns
+      // are in registers the next item may have them
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        const int t0 = 2 * i + odd, t1 = t0 + 2;
+        uint32_t d0[32], d1[32];
+        if (t0 < chunks) tmem_ld32(acc + (uint32_t)(32 * chunk(t0)), d0);
+        if (t1 < chunks) tmem_ld32(acc + (uint32_t)(32 * chunk(t1)), d1);
+        tmem_ld_wait();
+        if (i == 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(free_even);
+        }
+        if (t0 < chunks) store(d0, chunk(t0), xG[i]);
+        if (t1 < chunks) store(d1, chunk(t1), xG[i + 1]);
       }
-      ++n;
     }
   } else {
     // ---------------- scales: `which` 0 the weights', 1 and 2 the tokens' halves
@@ -279,8 +284,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
     const uint8_t *rowp[4];
     uint32_t cur[4][8];
     bool wanted = false;                                   // the second half of a narrow tile is not read
-    auto rows_of = [&](long long item) {
-      const MmItem m = mm_item<kPairRows>(a, groups, item, nrb);
+    Walk m(a, groups, nrb, first, step);
+    auto rows_of = [&]() {
       wanted = which < 2 || m.nrows > 128;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -309,12 +314,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
           if (it0 + i < nk) load_sf<WORDS>(rowp[j], it0 + i, a.nsf, a.sf_mode, fill, &cur[j][i * WORDS]);
       }
     };
-    long long item = first;
     int it0 = 0, s = 0, issued = 0;
     uint32_t ph = 0;
-    bool more = item < n_items;
+    bool more = m.more();
     if (more) {
-      rows_of(item);
+      rows_of();
       fetch(0);
     }
     bool failed = false;
@@ -329,9 +333,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
       it0 += Geo::AHEAD;
       if (it0 >= nk) {
         it0 = 0;
-        item += step;
-        more = item < n_items;
-        if (more) rows_of(item);
+        m.next(a, groups);
+        more = m.more();
+        if (more) rows_of();
       }
       if (more) fetch(it0);
 #pragma unroll
