@@ -34,9 +34,9 @@ inline int dtype_bytes(int32_t dt) {
 inline bool is_float_dtype(int32_t dt) { return dt == MOE_DT_F32 || dt == MOE_DT_BF16 || dt == MOE_DT_F16; }
 inline bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// The largest power of two up to 16 that divides a row's address at every row.
+// The largest power of two up to 32 that divides a row's address at every row.
 inline int row_alignment(const void *p, int64_t ld_bytes) {
-  const uintptr_t v = reinterpret_cast<uintptr_t>(p) | (uintptr_t)ld_bytes | 16u;
+  const uintptr_t v = reinterpret_cast<uintptr_t>(p) | (uintptr_t)ld_bytes | 32u;
   return (int)(v & (~v + 1));
 }
 
@@ -70,6 +70,23 @@ inline cudaError_t launch_op(void (*fn)(Args...), dim3 grid, int block, size_t s
   return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
+// Division of numbers below 2^31 by one that is known at launch: a multiplication
+// by m = ceil(2^(31 + l) / d), l = ceil(log2 d), is exact there (the hardware's own
+// 32-bit division takes three turns of the slow conversion pipe).
+struct FastDiv {
+  uint32_t d, m, s;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t d_) : d(d_), m(0), s(0) {
+    uint32_t l = 0;
+    while (((uint64_t)1 << l) < d) ++l;
+    if (l) {
+      m = (uint32_t)((((uint64_t)1 << (31 + l)) + d - 1) / d);
+      s = l - 1;
+    }
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t i) const { return d == 1 ? i : __umulhi(i, m) >> s; }
+};
+
 // ------------------------------------------------------------------ elements
 struct F32 {
   using raw = float;
@@ -87,31 +104,50 @@ struct F16 {
   static __device__ __forceinline__ raw from(float v) { return f16_bits(v); }
 };
 
-// N consecutive elements: one access when VEC (p is then aligned to the whole),
-// else N accesses, of which those at and behind `n` are left out.
-template <typename T, int N, bool VEC>
+// 32 bytes of one lane at once (sm_100): a whole sector, where two 16-byte accesses
+// at a 32-byte stride would touch every sector twice, half of it each time.
+__device__ __forceinline__ void ld32(const void *p, uint32_t *w) {
+  asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void st32(void *p, const uint32_t *w) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// N consecutive elements of a lane.  ALIGN is what every pack's address is a
+// multiple of: 32 or 16 bytes, or the element (0: one access an element).
+template <typename T, int N, int ALIGN>
 struct Pack {
   alignas(16) typename T::raw v[N];
-  __device__ __forceinline__ void load(const typename T::raw *p, int n) {
-    if constexpr (VEC) {
-      static_assert(sizeof(v) % 16 == 0, "whole 16-byte words");
-      uint4 *w = reinterpret_cast<uint4 *>(v);
+  static constexpr int kBytes = N * (int)sizeof(typename T::raw);
+  __device__ __forceinline__ void load(const typename T::raw *p) {
+    uint32_t *w = reinterpret_cast<uint32_t *>(v);
+    if constexpr (ALIGN == 32 && kBytes % 32 == 0) {
 #pragma unroll
-      for (int i = 0; i < (int)(sizeof(v) / 16); ++i) w[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+      for (int i = 0; i < kBytes / 32; ++i) ld32(reinterpret_cast<const char *>(p) + 32 * i, w + 8 * i);
+    } else if constexpr (ALIGN >= 16) {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i)
+        reinterpret_cast<uint4 *>(v)[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
     } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = i < n ? __ldg(p + i) : typename T::raw(0);
+      for (int i = 0; i < N; ++i) v[i] = __ldg(p + i);
     }
   }
-  __device__ __forceinline__ void store(typename T::raw *p, int n) const {
-    if constexpr (VEC) {
-      const uint4 *w = reinterpret_cast<const uint4 *>(v);
+  __device__ __forceinline__ void store(typename T::raw *p) const {
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(v);
+    if constexpr (ALIGN == 32 && kBytes % 32 == 0) {
 #pragma unroll
-      for (int i = 0; i < (int)(sizeof(v) / 16); ++i) reinterpret_cast<uint4 *>(p)[i] = w[i];
+      for (int i = 0; i < kBytes / 32; ++i) st32(reinterpret_cast<char *>(p) + 32 * i, w + 8 * i);
+    } else if constexpr (ALIGN >= 16) {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i) reinterpret_cast<uint4 *>(p)[i] = reinterpret_cast<const uint4 *>(v)[i];
     } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (i < n) p[i] = v[i];
+      for (int i = 0; i < N; ++i) p[i] = v[i];
     }
   }
   __device__ __forceinline__ float get(int i) const { return T::to(v[i]); }

@@ -7,11 +7,13 @@
 // Every rounding is that of the real quotient, with no double rounding:
 //  * 2^X is a power of two: v * 2^-X is exact.
 //  * The borders between codes, and between scales, have few digits: times d = s G
-//    (4 digits) or 6 G they are fp32 numbers, and a correctly rounded fp32 quotient
-//    lies on a border only where the real one does.  v / d is formed as q = v r,
-//    q' = q + (v - q d) r with r = 1 / d rounded: the residual of an fma is exact,
-//    and the corrected quotient is the correctly rounded one (Markstein 1990),
-//    for three multiply-adds an element instead of a division.
+//    (4 digits) or 6 G they are fp32 numbers, so a quotient that is not on a border
+//    is at least 0.53 ulp away from it, and the nearest fp32 number to it lies on
+//    the right side.  v / d is formed as q = v r, q' = q + (v - q d) r with r within
+//    an ulp or two of 1 / d: the residual of an fma is exact, q' is off by 2^-20 ulp
+//    before its rounding (Markstein 1990), so it is that nearest number, and a
+//    border exactly where the quotient is one: three multiply-adds an element, two
+//    elements an instruction, instead of a division.
 //
 // Bound by memory: x is read once and 0.53 or 0.56 bytes an element are written.
 // A thread takes 16 consecutive elements (one NVFP4 block, half an MXFP4 block).
@@ -20,13 +22,17 @@
 namespace moe {
 namespace {
 
-__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
+// Eight values to codes (round to nearest even, saturating), the first in bits 0..3.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
   uint32_t r;
-  asm("{\n\t.reg .b8 b;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\t"
-      "cvt.u32.u8 %0, b;\n\t}"
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
       : "=r"(r)
-      : "f"(lo), "f"(hi));
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return r;
 }
 __device__ __forceinline__ uint32_t e4m3_code(float v) {
@@ -34,21 +40,35 @@ __device__ __forceinline__ uint32_t e4m3_code(float v) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(v));
   return r & 0xFFu;
 }
-__device__ __forceinline__ float e4m3_value(uint32_t code) {
-  const uint32_t h2 = e4m3x2_to_f16x2((uint16_t)code);
-  return __half2float(__ushort_as_half((unsigned short)(h2 & 0xFFFFu)));
+// The value of a finite, non-negative code: its fields in place of a float's,
+// whose exponents lie 120 higher (exact for the subnormal codes too).
+__device__ __forceinline__ float e4m3_value(uint32_t code) { return __uint_as_float(code << 20) * 0x1p120f; }
+// The value of any code.
+__device__ __forceinline__ float e4m3_any(uint32_t code) {
+  const float v = e4m3_value(code & 127u);
+  return (code & 127u) == 127u ? __uint_as_float(0x7FC00000u) : code & 128u ? -v : v;
 }
 
 constexpr uint32_t kInfBits = 0x7F800000u;
 
 // Bits of the largest |v| (non-negative floats order like their bits; NaN and
 // infinity are at or above kInfBits).
-template <typename P>
-__device__ __forceinline__ uint32_t amax_bits16(const P &v) {
-  uint32_t m = 0;
+template <typename T, int ALIGN>
+__device__ __forceinline__ uint32_t amax_bits16(const Pack<T, 16, ALIGN> &v) {
+  if constexpr (sizeof(typename T::raw) == 4) {
+    uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v.get(i)) & 0x7FFFFFFFu);
-  return m;
+    for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v.get(i)) & 0x7FFFFFFFu);
+    return m;
+  } else {
+    // 16-bit magnitudes order like their bits too: two at a time
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(v.v);
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+    const uint32_t top = max(m & 0xFFFFu, m >> 16);
+    return __float_as_uint(T::to((uint16_t)top)) & 0x7FFFFFFFu;
+  }
 }
 
 // Bits of G for a group whose largest finite |v| has these bits: 2688 = 1.3125 *
@@ -59,22 +79,45 @@ __device__ __forceinline__ uint32_t global_bits(uint32_t amax) {
   return (uint32_t)max(ex, 127 - 100) << 23;
 }
 
-template <typename P>
-__device__ __forceinline__ uint2 codes_times(const P &v, float inv) {
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// Codes of 16 elements times `inv`, or, with DIV, divided by d (inv near 1 / d).
+template <bool DIV, typename P>
+__device__ __forceinline__ uint2 codes16(const P &v, float inv, float d) {
+  const uint64_t r = pack2(inv, inv), minus_d = pack2(-d, -d);
   uint32_t w[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    w[i] = 0;
+    float f[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[i] |= e2m1x2(v.get(8 * i + 2 * j) * inv, v.get(8 * i + 2 * j + 1) * inv) << (8 * j);
+    for (int j = 0; j < 4; ++j) {
+      const uint64_t x = pack2(v.get(8 * i + 2 * j), v.get(8 * i + 2 * j + 1));
+      uint64_t q = mul2(x, r);
+      if constexpr (DIV) q = fma2(fma2(q, minus_d, x), r, q);
+      asm("mov.b64 {%0, %1}, %2;" : "=f"(f[2 * j]), "=f"(f[2 * j + 1]) : "l"(q));
+    }
+    w[i] = e2m1x8(f);
   }
   return make_uint2(w[0], w[1]);
-}
-
-__device__ __forceinline__ float quotient(float v, float d, float r) {
-  const float q = v * r;
-  return fmaf(fmaf(-q, d, v), r, q);
 }
 
 // Scale code and codes of one NVFP4 block.
@@ -82,19 +125,13 @@ template <typename P>
 __device__ __forceinline__ uint32_t nv_block(const P &v, uint32_t amax, float G, uint2 *codes) {
   *codes = make_uint2(0u, 0u);
   if (amax >= kInfBits) return 0x7Fu;
-  const uint32_t sc = e4m3_code(__fdiv_rn(__uint_as_float(amax), 6.0f * G));
+  // amax / 6 correctly rounded (6's reciprocal is), then / G, a power of two
+  const float invG = __uint_as_float((254u << 23) - __float_as_uint(G));
+  const float top = __uint_as_float(amax), r6 = 1.0f / 6.0f, q6 = top * r6;
+  const uint32_t sc = e4m3_code(fmaf(fmaf(-6.0f, q6, top), r6, q6) * invG);
   if (sc == 0) return 0;
-  const float d = e4m3_value(sc) * G;
-  const float r = __frcp_rn(d);
-  uint32_t w[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    w[i] = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[i] |= e2m1x2(quotient(v.get(8 * i + 2 * j), d, r), quotient(v.get(8 * i + 2 * j + 1), d, r)) << (8 * j);
-  }
-  *codes = make_uint2(w[0], w[1]);
+  const float s = e4m3_value(sc);
+  *codes = codes16<true>(v, rcp_approx(s) * invG, s * G);
   return sc;
 }
 
@@ -105,67 +142,82 @@ struct FpArgs {
   float *G;
   int64_t ldx;               // elements
   uint32_t rows, cols16;     // cols16 = K / 16
+  FastDiv by_cols, by_group; // / cols16, / rows_per_scale
   uint32_t rows_per_scale;
   uint32_t total;            // rows * cols16, at most 2^31
 };
 
 // ------------------------------------------------------------------- quantise
-// One thread per 16 elements, flat over the rows.  MXFP4 halves meet by shuffle
-// (K is a multiple of 32, so a block's halves are neighbouring lanes).  NVFP4
-// finds its group's G in memory.
-template <typename T, bool VEC, bool MX>
+// A thread takes U pieces of 16 elements, flat over the rows, loads in flight
+// together.  MXFP4 halves meet by shuffle (K is a multiple of 32, so a block's
+// halves are neighbouring lanes); one piece a thread keeps HBM busy.  NVFP4 finds
+// its group's G in memory and does 1.5 times the work on a piece: with one piece a
+// thread its loads do not cover it (FLATU).
+template <typename T, int ALIGN, bool MX, int U>
 __global__ void __launch_bounds__(256) quantize_flat_kernel(const FpArgs a) {
   wait_prior_grid();
-  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
-  const bool in = i < a.total;
-  const uint32_t row = in ? i / a.cols16 : 0, c = in ? i - row * a.cols16 : 0;
-  Pack<T, 16, VEC> v;
-  v.load(static_cast<const typename T::raw *>(a.x) + row * a.ldx + 16 * c, in ? 16 : 0);
-  uint32_t am = amax_bits16(v);
-  if constexpr (MX) {
-    am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
-    uint32_t code = 1;
+  const uint32_t i0 = blockIdx.x * (256 * U) + threadIdx.x;
+  Pack<T, 16, ALIGN> v[U];
+  uint32_t row[U];
+  float G[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t i = i0 + 256 * u;
+    if (i < a.total) {
+      row[u] = a.by_cols.div(i);
+      v[u].load(static_cast<const typename T::raw *>(a.x) + row[u] * a.ldx + 16 * (i - row[u] * a.cols16));
+      if constexpr (!MX) G[u] = __ldcg(a.G + a.by_group.div(row[u]));
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t i = i0 + 256 * u;
+    const bool in = i < a.total;
+    uint32_t am = in ? amax_bits16(v[u]) : 0;
+    if constexpr (MX) am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+    if (!in) break;
     uint2 w = make_uint2(0u, 0u);
-    if (am >= kInfBits) {
-      code = 255;
+    if constexpr (MX) {
+      uint32_t code = 255;
+      if (am < kInfBits) {
+        code = (uint32_t)max(1, (int)(am >> 23) - 2);
+        w = codes16<false>(v[u], __uint_as_float((254u - code) << 23), 0.0f);
+      }
+      if ((i & 1) == 0) a.scales[i >> 1] = (uint8_t)code;
     } else {
-      code = (uint32_t)max(1, (int)(am >> 23) - 2);
-      w = codes_times(v, __uint_as_float((254u - code) << 23));
+      if (G[u] == 0.0f) {                              // nothing but zeros (and non-finite blocks) in the group
+        G[u] = 1.0f;
+        const uint32_t g = a.by_group.div(row[u]);
+        if (i == g * a.rows_per_scale * a.cols16) a.G[g] = 1.0f;
+      }
+      a.scales[i] = (uint8_t)nv_block(v[u], am, G[u], &w);
     }
-    if (!in) return;
     reinterpret_cast<uint2 *>(a.codes)[i] = w;
-    if ((i & 1) == 0) a.scales[i >> 1] = (uint8_t)code;
-  } else {
-    if (!in) return;
-    const uint32_t g = row / a.rows_per_scale;
-    float G = __ldcg(a.G + g);
-    if (G == 0.0f) {                                   // nothing but zeros (and non-finite blocks) in the group
-      G = 1.0f;
-      if (c == 0 && row == g * a.rows_per_scale) a.G[g] = 1.0f;
-    }
-    uint2 w;
-    const uint32_t sc = nv_block(v, am, G, &w);
-    reinterpret_cast<uint2 *>(a.codes)[i] = w;
-    a.scales[i] = (uint8_t)sc;
   }
 }
 
-// NVFP4 with a scale per row: the row's threads keep it in registers, agree on G
-// and quantise: one pass.  `tpr` threads (whole warps) to a row.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(1024) quantize_rows_kernel(const FpArgs a, int tpr) {
+// NVFP4 with a scale per row: the row's threads keep it in registers (NCH pieces
+// of 16 each), agree on G and quantise: one pass.  `tpr` threads (whole warps) to
+// a row; a row beyond what they hold (16384 elements and more) is read again for the codes.
+template <typename T, int ALIGN, int NCH>
+__global__ void __launch_bounds__(NCH == 1 ? 1024 : 512) quantize_rows_kernel(const FpArgs a, int tpr) {
   __shared__ uint32_t wmax[32];
   wait_prior_grid();
   const int rows_here = blockDim.x / tpr, lr = threadIdx.x / tpr, tc = threadIdx.x - lr * tpr;
   const uint64_t row = (uint64_t)blockIdx.x * rows_here + lr;
   const bool in = row < a.rows;
   const auto *x = static_cast<const typename T::raw *>(a.x) + (in ? row : 0) * a.ldx;
-  Pack<T, 16, VEC> v;
-  uint32_t am = 0, finite = 0;
-  for (uint32_t c = tc; c < a.cols16; c += tpr) {      // one turn up to 16 * 1024 columns
-    v.load(x + 16 * (uint64_t)c, in ? 16 : 0);
-    am = amax_bits16(v);
-    if (am < kInfBits) finite = max(finite, am);
+  Pack<T, 16, ALIGN> v[NCH];
+  uint32_t am[NCH], finite = 0;
+  for (uint32_t c0 = tc; c0 < a.cols16; c0 += NCH * tpr) {
+#pragma unroll
+    for (int i = 0; i < NCH; ++i)
+      if (in && c0 + i * tpr < a.cols16) v[i].load(x + 16 * (uint64_t)(c0 + i * tpr));
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      am[i] = in && c0 + i * tpr < a.cols16 ? amax_bits16(v[i]) : 0;
+      if (am[i] < kInfBits) finite = max(finite, am[i]);
+    }
   }
   finite = __reduce_max_sync(0xffffffffu, finite);
   if (tpr > 32) {
@@ -177,36 +229,52 @@ __global__ void __launch_bounds__(1024) quantize_rows_kernel(const FpArgs a, int
   if (!in) return;
   const float G = finite ? __uint_as_float(global_bits(finite)) : 1.0f;
   if (tc == 0) a.G[row] = G;
-  const bool one = a.cols16 <= (uint32_t)tpr;
-  for (uint32_t c = tc; c < a.cols16; c += tpr) {
-    if (!one) {
-      v.load(x + 16 * (uint64_t)c, 16);
-      am = amax_bits16(v);
+  const bool one = a.cols16 <= (uint32_t)(NCH * tpr);
+  for (uint32_t c0 = tc; c0 < a.cols16; c0 += NCH * tpr) {
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const uint32_t c = c0 + i * tpr;
+      if (c >= a.cols16) break;
+      if (!one) {
+        v[i].load(x + 16 * (uint64_t)c);
+        am[i] = amax_bits16(v[i]);
+      }
+      uint2 w;
+      const uint32_t sc = nv_block(v[i], am[i], G, &w);
+      const uint32_t at = (uint32_t)row * a.cols16 + c;
+      reinterpret_cast<uint2 *>(a.codes)[at] = w;
+      a.scales[at] = (uint8_t)sc;
     }
-    uint2 w;
-    const uint32_t sc = nv_block(v, am, G, &w);
-    const uint32_t i = (uint32_t)row * a.cols16 + c;
-    reinterpret_cast<uint2 *>(a.codes)[i] = w;
-    a.scales[i] = (uint8_t)sc;
   }
 }
 
 // NVFP4 with a scale per group of rows, first pass: G of every group.  G grows
 // with amax, so each CTA puts its own maximum's G into the group's word (zero
 // before) by an integer maximum, whose order does not matter.
-template <typename T, bool VEC>
+template <typename T, int ALIGN>
 __global__ void __launch_bounds__(256) group_scale_kernel(const FpArgs a, uint32_t per_group, uint32_t blocks) {
   __shared__ uint32_t wmax[8];
   wait_prior_grid();
   const uint32_t g = blockIdx.x / blocks, b = blockIdx.x - g * blocks;
   const uint32_t row0 = g * a.rows_per_scale;
   uint32_t finite = 0;
-  for (uint32_t i = b * 256 + threadIdx.x; i < per_group; i += blocks * 256) {
-    const uint32_t r = i / a.cols16, c = i - r * a.cols16;
-    Pack<T, 16, VEC> v;
-    v.load(static_cast<const typename T::raw *>(a.x) + (int64_t)(row0 + r) * a.ldx + 16 * c, 16);
-    const uint32_t am = amax_bits16(v);
-    if (am < kInfBits) finite = max(finite, am);
+  constexpr int U = sizeof(typename T::raw) == 4 ? 2 : 4;   // loads in flight together
+  const uint32_t step = blocks * 256;
+  for (uint32_t i = b * 256 + threadIdx.x; i < per_group; i += U * step) {
+    Pack<T, 16, ALIGN> v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t j = i + u * step;
+      if (j < per_group) {
+        const uint32_t r = a.by_cols.div(j);
+        v[u].load(static_cast<const typename T::raw *>(a.x) + (int64_t)(row0 + r) * a.ldx + 16 * (j - r * a.cols16));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t am = i + u * step < per_group ? amax_bits16(v[u]) : 0;
+      if (am < kInfBits) finite = max(finite, am);
+    }
   }
   finite = __reduce_max_sync(0xffffffffu, finite);
   if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = finite;
@@ -218,22 +286,37 @@ __global__ void __launch_bounds__(256) group_scale_kernel(const FpArgs a, uint32
 }
 
 // ----------------------------------------------------------------- dequantise
-template <typename T, bool VEC, bool MX>
+template <typename T, int ALIGN, bool MX>
 __global__ void __launch_bounds__(256) dequantize_kernel(const FpArgs a) {
   wait_prior_grid();
-  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= a.total) return;
-  const uint32_t row = i / a.cols16, c = i - row * a.cols16;
-  const uint2 w = __ldg(reinterpret_cast<const uint2 *>(a.codes) + i);
+  // four pieces a thread, their loads in flight together
+  const uint32_t i0 = blockIdx.x * 1024 + threadIdx.x;
+  uint2 code[4];
+  uint32_t scale[4], at[4];
+  float G[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const uint32_t i = i0 + 256 * u;
+    if (i >= a.total) break;
+    at[u] = a.by_cols.div(i);
+    code[u] = __ldg(reinterpret_cast<const uint2 *>(a.codes) + i);
+    scale[u] = __ldg(a.scales + (MX ? i >> 1 : i));
+    G[u] = MX ? 1.0f : __ldg(a.G + a.by_group.div(at[u]));
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+  const uint32_t i = i0 + 256 * u;
+  if (i >= a.total) break;
+  const uint32_t row = at[u], c = i - row * a.cols16;
+  const uint2 w = code[u];
   float d;
   if constexpr (MX) {
-    const uint32_t code = __ldg(a.scales + (i >> 1));
-    d = code == 255 ? __uint_as_float(0x7FC00000u)
-                    : code == 0 ? __uint_as_float(1u << 22) : __uint_as_float(code << 23);   // 0 is 2^-127
+    d = scale[u] == 255 ? __uint_as_float(0x7FC00000u)
+                        : scale[u] == 0 ? __uint_as_float(1u << 22) : __uint_as_float(scale[u] << 23);   // 0 is 2^-127
   } else {
-    d = e4m3_value(__ldg(a.scales + i)) * __ldg(a.G + row / a.rows_per_scale);
+    d = e4m3_any(scale[u]) * G[u];
   }
-  Pack<T, 16, VEC> out;
+  Pack<T, 16, ALIGN> out;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t f[4];
@@ -245,7 +328,8 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const FpArgs a) {
       out.set(8 * h + 2 * j + 1, p.y * d);
     }
   }
-  out.store(static_cast<typename T::raw *>(const_cast<void *>(a.x)) + row * a.ldx + 16 * c, 16);
+  out.store(static_cast<typename T::raw *>(const_cast<void *>(a.x)) + row * a.ldx + 16 * c);
+  }
 }
 
 moe_status_t check_fp4(const char *fn, int32_t dtype, int64_t rows, int64_t K, int64_t ld, int32_t fmt,
@@ -278,34 +362,47 @@ FpArgs fp_args(const void *x, int64_t rows, int64_t K, int64_t ld, int64_t rows_
   a.rows = (uint32_t)rows;
   a.cols16 = (uint32_t)(K / 16);
   a.rows_per_scale = (uint32_t)rows_per_scale;
+  a.by_cols = FastDiv(a.cols16);
+  a.by_group = FastDiv(a.rows_per_scale);
   a.total = a.rows * a.cols16;
   return a;
 }
 
-dim3 flat_grid(const FpArgs &a) { return dim3(a.total / 256 + (a.total % 256 != 0)); }
+// CTAs of 256 threads with `u` pieces to a thread.
+dim3 flat_grid(const FpArgs &a, uint32_t u) { return dim3(a.total / (256 * u) + (a.total % (256 * u) != 0)); }
 
-template <typename T, bool VEC>
+template <typename T, int ALIGN>
 cudaError_t quantize(const FpArgs &a, int32_t fmt, cudaStream_t s) {
-  if (fmt == MOE_FMT_MXFP4) return launch_op(quantize_flat_kernel<T, VEC, true>, flat_grid(a), 256, 0, s, a);
+  if (fmt == MOE_FMT_MXFP4) return launch_op(quantize_flat_kernel<T, ALIGN, true, 1>, flat_grid(a, 1), 256, 0, s, a);
   if (a.rows_per_scale == 1) {
-    const int tpr = (int)std::min<uint32_t>(1024, (a.cols16 + 31) / 32 * 32);
+    // few rows: a thread takes one piece, so that a row is spread wide; rows that
+    // fill the GPU: as many as leave every lane of a row's warp one (four, of fp32
+    // two, at most), whose loads are in flight together
+    constexpr uint32_t kMost = sizeof(typename T::raw) == 4 ? 2 : 4;
+    const uint32_t nch = a.total < (uint32_t)(sm_count() * 2048) || a.cols16 <= 32 ? 1
+                         : a.cols16 <= 64                                         ? 2
+                                                                                  : kMost;
+    const int tpr = (int)std::min<uint32_t>(nch > 1 ? 512 : 1024, ((a.cols16 + nch - 1) / nch + 31) / 32 * 32);
     const int rows_here = std::max(1, 256 / tpr);
-    return launch_op(quantize_rows_kernel<T, VEC>, dim3((a.rows + rows_here - 1) / rows_here), tpr * rows_here, 0, s, a,
-                     tpr);
+    return launch_op(nch == 1   ? quantize_rows_kernel<T, ALIGN, 1>
+                     : nch == 2 ? quantize_rows_kernel<T, ALIGN, 2>
+                                : quantize_rows_kernel<T, ALIGN, kMost>,
+                     dim3((a.rows + rows_here - 1) / rows_here), tpr * rows_here, 0, s, a, tpr);
   }
+  constexpr uint32_t kFlat = sizeof(typename T::raw) == 4 ? 2 : 4;
   const uint32_t groups = a.rows / a.rows_per_scale, per_group = a.rows_per_scale * a.cols16;
   const uint32_t want = std::max<uint32_t>(1, (uint32_t)(8 * sm_count()) / groups);
-  const uint32_t blocks = std::min<uint32_t>(want, (per_group + 1023) / 1024);
+  const uint32_t blocks = std::min<uint32_t>(want, (per_group + 1023) / 1024);   // four turns of a CTA at least
   cudaError_t e = cudaMemsetAsync(a.G, 0, (size_t)groups * sizeof(float), s);
-  if (e == cudaSuccess) e = launch_op(group_scale_kernel<T, VEC>, dim3(groups * blocks), 256, 0, s, a, per_group, blocks);
-  if (e == cudaSuccess) e = launch_op(quantize_flat_kernel<T, VEC, false>, flat_grid(a), 256, 0, s, a);
+  if (e == cudaSuccess) e = launch_op(group_scale_kernel<T, ALIGN>, dim3(groups * blocks), 256, 0, s, a, per_group, blocks);
+  if (e == cudaSuccess) e = launch_op(quantize_flat_kernel<T, ALIGN, false, kFlat>, flat_grid(a, kFlat), 256, 0, s, a);
   return e;
 }
 
-template <typename T, bool VEC>
+template <typename T, int ALIGN>
 cudaError_t dequantize(const FpArgs &a, int32_t fmt, cudaStream_t s) {
-  return launch_op(fmt == MOE_FMT_MXFP4 ? dequantize_kernel<T, VEC, true> : dequantize_kernel<T, VEC, false>,
-                   flat_grid(a), 256, 0, s, a);
+  return launch_op(fmt == MOE_FMT_MXFP4 ? dequantize_kernel<T, ALIGN, true> : dequantize_kernel<T, ALIGN, false>,
+                   flat_grid(a, 4), 256, 0, s, a);
 }
 
 }  // namespace
@@ -313,10 +410,11 @@ cudaError_t dequantize(const FpArgs &a, int32_t fmt, cudaStream_t s) {
 
 using namespace moe;
 
-#define MOE_BY_TYPE(f)                                                                       \
-  (dtype == MOE_DT_F32    ? (vec ? f<F32, true>(a, fmt, s) : f<F32, false>(a, fmt, s))       \
-   : dtype == MOE_DT_BF16 ? (vec ? f<BF16, true>(a, fmt, s) : f<BF16, false>(a, fmt, s))     \
-                          : (vec ? f<F16, true>(a, fmt, s) : f<F16, false>(a, fmt, s)))
+#define MOE_BY_ALIGN(f, T) (al == 32 ? f<T, 32>(a, fmt, s) : al == 16 ? f<T, 16>(a, fmt, s) : f<T, 0>(a, fmt, s))
+#define MOE_BY_TYPE(f)                                    \
+  (dtype == MOE_DT_F32    ? MOE_BY_ALIGN(f, F32)          \
+   : dtype == MOE_DT_BF16 ? MOE_BY_ALIGN(f, BF16)         \
+                          : MOE_BY_ALIGN(f, F16))
 
 extern "C" {
 
@@ -328,7 +426,7 @@ moe_status_t moe_fp4_quantize(const void *x, int32_t dtype, int64_t rows, int64_
   if (st != MOE_OK || rows == 0) return st;
   const FpArgs a = fp_args(x, rows, K, ldx, rows_per_scale, codes, scales, global_scale);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool vec = row_alignment(x, ldx * dtype_bytes(dtype)) == 16;
+  const int al = row_alignment(x, ldx * dtype_bytes(dtype));
   return ops_launched(fn, MOE_BY_TYPE(quantize));
 }
 
@@ -340,7 +438,7 @@ moe_status_t moe_fp4_dequantize(const uint8_t *codes, const uint8_t *scales, con
   if (st != MOE_OK || rows == 0) return st;
   const FpArgs a = fp_args(out, rows, K, ldo, rows_per_scale, codes, scales, global_scale);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool vec = row_alignment(out, ldo * dtype_bytes(dtype)) == 16;
+  const int al = row_alignment(out, ldo * dtype_bytes(dtype));
   return ops_launched(fn, MOE_BY_TYPE(dequantize));
 }
 

@@ -496,7 +496,7 @@ extern "C" moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_
               : a.nsf % 4 == 0 && aligned_to(x_scales, 4) && aligned_to(w_scales, 4)           ? 1
                                                                                               : 2;
   a.sf_wide = a.sf_mode == 0 && a.nsf % 16 == 0 && aligned_to(x_scales, 16) && aligned_to(w_scales, 16);
-  a.y_vec = row_alignment(y, ldy * dtype_bytes(dtype)) == 16;
+  a.y_vec = row_alignment(y, ldy * dtype_bytes(dtype)) >= 16;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (pairs)
     return ops_launched(fn, launch_matmul_pair(fmt == MOE_FMT_MXFP4 ? WF_MX : WF_NV, a,

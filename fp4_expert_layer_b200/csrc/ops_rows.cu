@@ -262,7 +262,7 @@ moe_status_t check_shape(const char *fn, int32_t T, int32_t k, int32_t H, int32_
   return MOE_OK;
 }
 
-bool vec_rows(const void *p, int64_t ld, int32_t dt) { return !p || row_alignment(p, ld * dtype_bytes(dt)) == 16; }
+bool vec_rows(const void *p, int64_t ld, int32_t dt) { return !p || row_alignment(p, ld * dtype_bytes(dt)) >= 16; }
 
 }  // namespace
 }  // namespace moe
@@ -290,7 +290,7 @@ moe_status_t moe_dispatch(const void *x, int32_t dtype, int32_t T, int32_t k, in
   a.T = T; a.k = k; a.rows = rows;
   const int64_t row_bytes = (int64_t)H * es;
   // the widest unit that every row starts and ends on
-  const int v = std::min({row_alignment(x, a.ldx), row_alignment(xs, a.ldxs), row_alignment(nullptr, row_bytes)});
+  const int v = std::min({16, row_alignment(x, a.ldx), row_alignment(xs, a.ldxs), row_alignment(nullptr, row_bytes)});
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = v == 16  ? launch_dispatch<uint4>(a, row_bytes, s)
                   : v == 8 ? launch_dispatch<uint2>(a, row_bytes, s)
