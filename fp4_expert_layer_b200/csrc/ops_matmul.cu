@@ -38,7 +38,6 @@ constexpr int kMmThreads = 320;
 template <int WF, int NT>
 struct MmGeom {
   static constexpr int NBLK = (WF == WF_MX) ? 2 : 4;       // 4-scale blocks of 256 K
-  static constexpr int WORDS = NBLK;                       // 32-bit words of scales a row has in a stage
   static constexpr int SF_BYTES = NBLK * 512;
   static constexpr int A_BYTES = 128 * 128;
   static constexpr int B_BYTES = NT * 128;
@@ -59,7 +58,7 @@ struct MmGeom {
 template <int WF, int NT, bool SPLIT>
 __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_constant__ MatmulArgs a) {
   using Geo = MmGeom<WF, NT>;
-  constexpr int S = Geo::STAGES, NBUF = Geo::NBUF, WORDS = Geo::WORDS;
+  constexpr int S = Geo::STAGES, NBUF = Geo::NBUF, WORDS = kSfWords<WF>;
   extern __shared__ __align__(1024) uint8_t mm_raw[];
   __shared__ __align__(8) uint64_t full_bar[S];
   __shared__ __align__(8) uint64_t empty_bar[S];
@@ -220,75 +219,34 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
       }
     }
   } else {
-    // ---------------- scales: pair p = (warp - 6) / 2 takes the stages with
-    // (stage count) % 2 == p.  Row words are loaded one stage of the pair ahead.
-    const int pair = (warp - 6) >> 1;
+    // ---------------- scales: warps 6 and 8 the weights', 7 and 9 the tokens', on
+    // alternate steps
     const bool tokens = (warp & 1) != 0;
-    const uint32_t fill = kSfOne<WF>;
     constexpr int RG = (NT + 31) / 32 < 4 ? (NT + 31) / 32 : 4;        // 32-row groups of a token tile
-    // the (item, stage) sequence this warp loads, and where it stores
-    Walk m(a, groups, nrb, first, step);
-    int it = k0, seq = 0;
-    bool have = m.more() && k1 > k0;
     const uint8_t *rowp[4];
-    auto rows_of = [&]() {
+    const uint32_t off = Geo::SF_OFF + (tokens ? Geo::SF_BYTES : 0) + 16 * lane;
+    feed_scales<WF, S>(
+        a, groups, Walk(a, groups, nrb, first, step), k0, k1, (warp - 6) >> 1, 2,
+        [&](const Walk &m) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (tokens) {
-          const int r = min(m.row0 + 32 * j + lane, a.rows - 1);
-          rowp[j] = a.xs + (size_t)r * a.nsf;
-        } else {
-          const int r = min(m.rb * 128 + 32 * j + lane, a.N - 1);
-          rowp[j] = a.ws + ((size_t)m.g * a.N + r) * a.nsf;
-        }
-      }
-    };
-    if (have) rows_of();
-    auto advance = [&]() {
-      ++seq;
-      if (++it == k1) {
-        it = k0;
-        m.next(a, groups);
-        have = m.more();
-        if (have) rows_of();
-      }
-    };
-    uint32_t cur[4][WORDS];
-    auto fetch = [&]() {
+          for (int j = 0; j < 4; ++j)
+            rowp[j] = tokens ? a.xs + (size_t)min(m.row0 + 32 * j + lane, a.rows - 1) * a.nsf
+                             : a.ws + ((size_t)m.g * a.N + min(m.rb * 128 + 32 * j + lane, a.N - 1)) * a.nsf;
+        },
+        [&](int it0, uint32_t(&w)[4][8]) { fetch_sf<WF>(a, rowp, tokens ? RG : 4, it0, k1, w); },
+        [&](int s, uint32_t parity) { return mbar_wait_warp(smem_u32(&empty_bar[s]), parity, a.err, 65); },
+        [&](const Walk &) {
+          return [&](int s, const uint32_t(&w)[4][8], int i) {
+            const uint32_t dst = smem_u32(smem + (size_t)s * Geo::STAGE) + off;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (!tokens || j < RG) {
-          load_sf<WORDS>(rowp[j], it, a.nsf, a.sf_mode, fill, cur[j]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < WORDS; ++i) cur[j][i] = fill;
-        }
-      }
-    };
-    if (pair == 1 && have) advance();
-    bool loaded = have;
-    if (have) fetch();
-    while (loaded) {
-      const int s = seq % S;
-      const int round = seq / S;
-      uint32_t hold[4][WORDS];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < WORDS; ++i) hold[j][i] = cur[j][i];
-      advance();                                           // past the other pair's stage, to the next of this one
-      if (have) advance();
-      loaded = have;
-      if (have) fetch();
-      if (round > 0 && !mbar_wait_warp(smem_u32(&empty_bar[s]), (round - 1) & 1, a.err, 65)) break;
-      const uint32_t dst = smem_u32(smem + (size_t)s * Geo::STAGE) + Geo::SF_OFF + (tokens ? Geo::SF_BYTES : 0) + 16 * lane;
-#pragma unroll
-      for (int b = 0; b < WORDS; ++b)
-        sts128(dst + 512 * b, make_uint4(hold[0][b], hold[1][b], hold[2][b], hold[3][b]));
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&full_bar[s]));
-    }
+            for (int b = 0; b < WORDS; ++b)                // rows past the tile's: any number, their columns go nowhere
+              sts128(dst + 512 * b, make_uint4(w[0][i * WORDS + b], w[1][i * WORDS + b], w[2][i * WORDS + b],
+                                               w[3][i * WORDS + b]));
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&full_bar[s]));
+          };
+        });
   }
 
   if constexpr (SPLIT) {

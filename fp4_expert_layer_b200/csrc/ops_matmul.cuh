@@ -142,6 +142,76 @@ __device__ __forceinline__ void load_sf(const uint8_t *row, int it, int nsf, int
 template <int WF>
 constexpr uint32_t kSfOne = WF == WF_MX ? 0x7F7F7F7Fu : 0x38383838u;
 
+// Scales come 32 bytes of a row at a time, a whole sector of memory: AHEAD stages.
+template <int WF>
+constexpr int kSfWords = WF == WF_MX ? 2 : 4;              // words of scales a row has in a stage
+template <int WF>
+constexpr int kSfAhead = 8 / kSfWords<WF>;
+
+// 32 bytes of four rows' scales from stage it0 on (as far as stage k1).
+template <int WF>
+__device__ __forceinline__ void fetch_sf(const MatmulArgs &a, const uint8_t *const (&row)[4], int rows, int it0, int k1,
+                                         uint32_t (&w)[4][8]) {
+  constexpr int WORDS = kSfWords<WF>, AHEAD = kSfAhead<WF>;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (j >= rows) break;
+    if (a.sf_wide && it0 + AHEAD <= k1) {
+      const uint4 *p = reinterpret_cast<const uint4 *>(row[j] + it0 * 4 * WORDS);
+      const uint4 lo = __ldg(p), hi = __ldg(p + 1);
+      w[j][0] = lo.x; w[j][1] = lo.y; w[j][2] = lo.z; w[j][3] = lo.w;
+      w[j][4] = hi.x; w[j][5] = hi.y; w[j][6] = hi.z; w[j][7] = hi.w;
+      continue;
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      if (it0 + i < k1) load_sf<WORDS>(row[j], it0 + i, a.nsf, a.sf_mode, kSfOne<WF>, &w[j][i * WORDS]);
+  }
+}
+
+// A scale warp's work: of the sequence (item, steps of AHEAD stages in [k0, k1)) it
+// takes every `stride`-th step from `phase` on, loads the next of them while it
+// stores the last.  rows_of(walk) sets the row pointers of an item; put(s, stage's
+// words, i) stores one stage's blocks into ring place s and arrives.
+template <int WF, int S, typename Walk, typename RowsOf, typename Fetch, typename Wait, typename Put>
+__device__ __forceinline__ void feed_scales(const MatmulArgs &a, const MmGroups &t, Walk m, int k0, int k1, int phase,
+                                            int stride, RowsOf rows_of, Fetch fetch, Wait wait_empty, Put put) {
+  constexpr int AHEAD = kSfAhead<WF>;
+  int it0 = k0, seq = 0;                                   // seq: stages before this step, over all items
+  bool more = m.more() && k1 > k0;
+  auto advance = [&]() {
+    seq += min(AHEAD, k1 - it0);
+    it0 += AHEAD;
+    if (it0 < k1) return;
+    it0 = k0;
+    m.next(a, t);
+    more = m.more();
+    if (more) rows_of(m);
+  };
+  if (more) rows_of(m);
+  for (int i = 0; i < phase && more; ++i) advance();
+  uint32_t cur[4][8];
+  if (more) fetch(it0, cur);
+  while (more) {
+    uint32_t hold[4][8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) hold[j][i] = cur[j][i];
+    const int stages = min(AHEAD, k1 - it0), first = seq;
+    const auto ticket = put(m);                            // what put has to know of the step's item
+    for (int i = 0; i < stride && more; ++i) advance();
+    if (more) fetch(it0, cur);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      if (i >= stages) break;
+      const int s = (first + i) % S, round = (first + i) / S;
+      if (round > 0 && !wait_empty(s, (round - 1) & 1)) return;
+      ticket(s, hold, i);
+    }
+  }
+}
+
 __device__ __forceinline__ void store_out(void *y, int dtype, int64_t at, float v) {
   if (dtype == MOE_DT_F32) static_cast<float *>(y)[at] = v;
   else if (dtype == MOE_DT_BF16) static_cast<uint16_t *>(y)[at] = bf16_bits(v);

@@ -37,8 +37,6 @@ constexpr int kPairEpi = 8;                                // epilogue warps of 
 template <int WF>
 struct PairGeom {
   static constexpr int NBLK = (WF == WF_MX) ? 2 : 4;       // 4-scale blocks of 256 K
-  static constexpr int WORDS = NBLK;                       // words of scales a row has in a stage
-  static constexpr int AHEAD = 8 / WORDS;                  // stages that 32 bytes of a row's scales are
   static constexpr int A_BYTES = 128 * 128;
   static constexpr int BOX_BYTES = kPairBox * 128;
   static constexpr int SFA_OFF = 2 * A_BYTES;              // codes: 128 weight rows, then 128 token rows
@@ -56,7 +54,7 @@ struct PairGeom {
 template <int WF>
 __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const __grid_constant__ MatmulArgs a) {
   using Geo = PairGeom<WF>;
-  constexpr int S = Geo::STAGES, WORDS = Geo::WORDS, NBLK = Geo::NBLK;
+  constexpr int S = Geo::STAGES, WORDS = kSfWords<WF>, NBLK = Geo::NBLK;
   extern __shared__ __align__(1024) uint8_t pm_raw[];
   __shared__ __align__(8) uint64_t full_bar[S];            // the even CTA's: both CTAs' copies and scales
   __shared__ __align__(8) uint64_t empty_bar[S];           // each CTA's: the MMAs of the stage are done
@@ -278,84 +276,36 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
   } else {
     // ---------------- scales: `which` 0 the weights', 1 and 2 the tokens' halves
     const int which = warp - (2 + kPairEpi);
-    const int off = which == 0 ? Geo::SFA_OFF : Geo::SFB_OFF + 512 * (which - 1);
+    const uint32_t off = (which == 0 ? Geo::SFA_OFF : Geo::SFB_OFF + 512 * (which - 1)) + 16 * lane;
     const int pitch = which == 0 ? 512 : 1024;             // between a stage's blocks
-    const uint32_t fill = kSfOne<WF>;
     const uint8_t *rowp[4];
-    uint32_t cur[4][8];
     bool wanted = false;                                   // the second half of a narrow tile is not read
-    Walk m(a, groups, nrb, first, step);
-    auto rows_of = [&]() {
-      wanted = which < 2 || m.nrows > 128;
+    feed_scales<WF, S>(
+        a, groups, Walk(a, groups, nrb, first, step), 0, nk, 0, 1,
+        [&](const Walk &m) {
+          wanted = which < 2 || m.nrows > 128;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (which == 0) {
-          const int r = min(m.rb * 256 + (int)rank * 128 + 32 * j + lane, a.N - 1);
-          rowp[j] = a.ws + ((size_t)m.g * a.N + r) * a.nsf;
-        } else {
-          const int r = min(m.row0 + 128 * (which - 1) + 32 * j + lane, a.rows - 1);
-          rowp[j] = a.xs + (size_t)r * a.nsf;
-        }
-      }
-    };
-    auto fetch = [&](int it0) {                            // 32 bytes of each row, from stage it0 on
-      if (!wanted) return;
+          for (int j = 0; j < 4; ++j)
+            rowp[j] = which == 0
+                          ? a.ws + ((size_t)m.g * a.N + min(m.rb * 256 + (int)rank * 128 + 32 * j + lane, a.N - 1)) * a.nsf
+                          : a.xs + (size_t)min(m.row0 + 128 * (which - 1) + 32 * j + lane, a.rows - 1) * a.nsf;
+        },
+        [&](int it0, uint32_t(&w)[4][8]) { fetch_sf<WF>(a, rowp, wanted ? 4 : 0, it0, nk, w); },
+        [&](int s, uint32_t parity) { return mbar_wait_warp(smem_u32(&empty_bar[s]), parity, a.err, 75); },
+        [&](const Walk &) {
+          return [&, store = wanted](int s, const uint32_t(&w)[4][8], int i) {
+            if (store) {
+              const uint32_t dst = smem_u32(smem + (size_t)s * Geo::STAGE) + off;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (a.sf_wide && it0 + Geo::AHEAD <= nk) {
-          const uint4 *p = reinterpret_cast<const uint4 *>(rowp[j] + it0 * 4 * WORDS);
-          const uint4 lo = __ldg(p), hi = __ldg(p + 1);
-          cur[j][0] = lo.x; cur[j][1] = lo.y; cur[j][2] = lo.z; cur[j][3] = lo.w;
-          cur[j][4] = hi.x; cur[j][5] = hi.y; cur[j][6] = hi.z; cur[j][7] = hi.w;
-          continue;
-        }
-#pragma unroll
-        for (int i = 0; i < Geo::AHEAD; ++i)
-          if (it0 + i < nk) load_sf<WORDS>(rowp[j], it0 + i, a.nsf, a.sf_mode, fill, &cur[j][i * WORDS]);
-      }
-    };
-    int it0 = 0, s = 0, issued = 0;
-    uint32_t ph = 0;
-    bool more = m.more();
-    if (more) {
-      rows_of();
-      fetch(0);
-    }
-    bool failed = false;
-    while (more && !failed) {
-      uint32_t hold[4][8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) hold[j][i] = cur[j][i];
-      const int stages = min(Geo::AHEAD, nk - it0);
-      const bool put = wanted;
-      it0 += Geo::AHEAD;
-      if (it0 >= nk) {
-        it0 = 0;
-        m.next(a, groups);
-        more = m.more();
-        if (more) rows_of();
-      }
-      if (more) fetch(it0);
-#pragma unroll
-      for (int i = 0; i < Geo::AHEAD; ++i) {
-        if (i >= stages || failed) break;
-        if (issued >= S && !mbar_wait_warp(smem_u32(&empty_bar[s]), ph ^ 1u, a.err, 75)) { failed = true; break; }
-        if (put) {
-          const uint32_t dst = smem_u32(smem + (size_t)s * Geo::STAGE) + off + 16 * lane;
-#pragma unroll
-          for (int b = 0; b < WORDS; ++b)
-            sts128(dst + pitch * b, make_uint4(hold[0][i * WORDS + b], hold[1][i * WORDS + b], hold[2][i * WORDS + b],
-                                               hold[3][i * WORDS + b]));
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-        }
-        if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&full_bar[s]), 0));
-        ++issued;
-        if (++s == S) { s = 0; ph ^= 1u; }
-      }
-    }
+              for (int b = 0; b < WORDS; ++b)
+                sts128(dst + pitch * b, make_uint4(w[0][i * WORDS + b], w[1][i * WORDS + b], w[2][i * WORDS + b],
+                                                   w[3][i * WORDS + b]));
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              __syncwarp();
+            }
+            if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&full_bar[s]), 0));
+          };
+        });
   }
 
   __syncwarp();
