@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 #include <string>
 
 #include "device_utils.cuh"
@@ -40,7 +41,7 @@ inline int row_alignment(const void *p, int64_t ld_bytes) {
   return (int)(v & (~v + 1));
 }
 
-// The current device and its SM count, looked up once per device.
+// The current device's SM count, looked up once per device.
 inline int sm_count() {
   static int n[64] = {};
   int dev = 0;
@@ -50,6 +51,20 @@ inline int sm_count() {
     n[dev] = cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && v > 0 ? v : 148;
   }
   return n[dev];
+}
+
+// Shared memory above 48 KB has to be asked for, once per kernel and device
+// (`asked`: a bit for each device, kept beside the kernel's launch).
+template <typename... Args>
+inline cudaError_t ask_shared(void (*fn)(Args...), size_t bytes, std::atomic<uint64_t> &asked) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = (uint64_t)1 << (dev & 63);
+  if (dev < 64 && (asked.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev < 64) asked.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // A launch that may start while its predecessor on the stream drains; the

@@ -346,7 +346,8 @@ template <int WF, int NT, bool SPLIT>
 cudaError_t launch_matmul(const MatmulArgs &a, int grid, int ranks, cudaStream_t s) {
   using Geo = MmGeom<WF, NT>;
   auto fn = fp4_matmul_kernel<WF, NT, SPLIT>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Geo::SMEM);
+  static std::atomic<uint64_t> asked{0};
+  const cudaError_t e = ask_shared(fn, Geo::SMEM, asked);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(grid * ranks));

@@ -321,7 +321,8 @@ template <int WF>
 cudaError_t launch_pair(const MatmulArgs &a, int pairs, cudaStream_t s) {
   using Geo = PairGeom<WF>;
   auto fn = fp4_matmul_pair_kernel<WF>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Geo::SMEM);
+  static std::atomic<uint64_t> asked{0};
+  const cudaError_t e = ask_shared(fn, Geo::SMEM, asked);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * pairs));

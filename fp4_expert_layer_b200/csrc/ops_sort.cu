@@ -270,8 +270,8 @@ cudaError_t sort_by_cluster(const SortArgs &a, cudaStream_t s) {
   int W = 4;
   while (W < 16 && W * C < steps) W *= 2;
   static_assert((16 + 2) * kMaxExperts * 4 + 128 <= 227 * 1024, "histograms fit a CTA");
-  cudaError_t e = cudaFuncSetAttribute(sort_pairs_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sort_smem(kMaxExperts, 16));
+  static std::atomic<uint64_t> asked{0};
+  cudaError_t e = ask_shared(sort_pairs_kernel, sort_smem(kMaxExperts, 16), asked);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)C);
@@ -296,8 +296,8 @@ cudaError_t sort_by_chunks(SortArgs a, cudaStream_t s) {
   a.chunk = std::max(least, ((a.n + most - 1) / most + 31) / 32 * 32);
   a.chunks = std::max(1, a.n / a.chunk);
   const size_t smem = sort_smem(a.E, kChunkThreads / 32);
-  cudaError_t e = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sort_smem(kMaxExperts, kChunkThreads / 32));
+  static std::atomic<uint64_t> asked{0};
+  cudaError_t e = ask_shared(sort_place_kernel, sort_smem(kMaxExperts, kChunkThreads / 32), asked);
   if (e == cudaSuccess) e = launch_op(sort_count_kernel, dim3(a.chunks), kChunkThreads, 0, s, a);
   if (e == cudaSuccess) e = launch_op(sort_scan_kernel, dim3((a.E + 31) / 32), 1024, 0, s, a);
   if (e == cudaSuccess) e = launch_op(sort_place_kernel, dim3(a.chunks), kChunkThreads, smem, s, a);

@@ -85,10 +85,12 @@ def _same(fn, dev, *tensors):
 
 def _ld(fn, name, t, rows, cols):
     """Row stride of a 2-D tensor with contiguous rows."""
+    if t.is_contiguous():
+        return cols
     ld, inner = t.stride()
     if cols > 1 and inner != 1:
         _bad(f"{fn}: the rows of {name} must be contiguous")
-    return ld if rows > 1 else max(cols, 1)
+    return ld if rows > 1 else cols
 
 
 def _float(fn, name, t):
@@ -166,9 +168,11 @@ def fp4_quantize(x, fmt="mxfp4", rows_per_scale=None, out=None, stream=None):
         codes, scales, g = out.codes, out.scales, out.global_scale
         if nv:
             _want(fn, "out.global_scale", g, _F32, (n // per,))
-    check(lib().moe_fp4_quantize(x2.data_ptr(), _float(fn, "x", x), n, K, _ld(fn, "x", x2, n, K), 1 if nv else 0, per,
+    status = lib().moe_fp4_quantize(x2.data_ptr(), _float(fn, "x", x), n, K, _ld(fn, "x", x2, n, K), 1 if nv else 0, per,
                                  codes.data_ptr(), scales.data_ptr(), g.data_ptr() if nv else None,
-                                 _raw_stream(dev)))
+                                 _raw_stream(dev))
+    if status:
+        check(status)
     return out
 
 
@@ -197,9 +201,11 @@ def fp4_dequantize(q, dtype=torch.float32, out=None, stream=None):
             _bad(f"{fn}: out must be {[*lead, K]}, contiguous if it has three axes, not {list(out.shape)}")
         _same(fn, dev, out)
         o2 = out if len(lead) == 1 else out.view(n, K)
-    check(lib().moe_fp4_dequantize(codes.data_ptr(), scales.data_ptr(), None if g is None else g.data_ptr(), fmt, n, K,
+    status = lib().moe_fp4_dequantize(codes.data_ptr(), scales.data_ptr(), None if g is None else g.data_ptr(), fmt, n, K,
                                    per, o2.data_ptr(), _float(fn, "out", o2), _ld(fn, "out", o2, n, K),
-                                   _raw_stream(dev)))
+                                   _raw_stream(dev))
+    if status:
+        check(status)
     return out
 
 
@@ -237,10 +243,12 @@ def fp4_matmul(x, w, offsets=None, out_dtype=torch.bfloat16, out=None, stream=No
         if out.shape != (n, N):
             _bad(f"{fn}: out must be [{n}, {N}], not {list(out.shape)}")
         _same(fn, dev, out)
-    check(lib().moe_fp4_matmul(xc.data_ptr(), xs.data_ptr(), xg.data_ptr() if fmt else None, n, wc.data_ptr(),
+    status = lib().moe_fp4_matmul(xc.data_ptr(), xs.data_ptr(), xg.data_ptr() if fmt else None, n, wc.data_ptr(),
                                ws.data_ptr(), wg.data_ptr() if fmt else None, groups, N, K, fmt,
                                None if offsets is None else offsets.data_ptr(), out.data_ptr(),
-                               _float(fn, "out", out), _ld(fn, "out", out, n, N), _raw_stream(dev)))
+                               _float(fn, "out", out), _ld(fn, "out", out, n, N), _raw_stream(dev))
+    if status:
+        check(status)
     return out
 
 
@@ -261,8 +269,10 @@ def sort_tokens(ids, n_experts, stream=None):
         _bad(f"sort_tokens: {E} experts: 1 to 1024 are supported")
     counts, offsets = _empty_strided((E,), (1,), _I32), _empty_strided((E + 1,), (1,), _I32)
     perm, inv = _empty_strided((T * k,), (1,), _I32), _new(T, k, _I32)
-    check(lib().moe_sort_tokens(ids.data_ptr(), T, k, E, counts.data_ptr(), offsets.data_ptr(), perm.data_ptr(),
-                                inv.data_ptr(), _raw_stream(dev)))
+    status = lib().moe_sort_tokens(ids.data_ptr(), T, k, E, counts.data_ptr(), offsets.data_ptr(), perm.data_ptr(),
+                                inv.data_ptr(), _raw_stream(dev))
+    if status:
+        check(status)
     return {"counts": counts, "offsets": offsets, "perm": perm, "inv": inv}
 
 
@@ -312,8 +322,10 @@ def dispatch(x, inv, rows=None, out=None, stream=None):
     else:
         rows = out.shape[0] if rows is None else rows
         _out(fn, out, dtype, rows, H, dev)
-    check(lib().moe_dispatch(x.data_ptr(), dt, T, k, H, _ld(fn, "x", x, T, H), inv.data_ptr(), rows, out.data_ptr(),
-                             _ld(fn, "out", out, rows, H), _raw_stream(dev)))
+    status = lib().moe_dispatch(x.data_ptr(), dt, T, k, H, _ld(fn, "x", x, T, H), inv.data_ptr(), rows, out.data_ptr(),
+                             _ld(fn, "out", out, rows, H), _raw_stream(dev))
+    if status:
+        check(status)
     return out
 
 
@@ -327,8 +339,10 @@ def dispatch_backward(dxs, inv, out=None, stream=None):
     T, k = _pairs(fn, inv, None, dev)
     dt = _float(fn, "dxs", dxs)
     out = _new(T, H, dxs.dtype) if out is None else _out(fn, out, dxs.dtype, T, H, dev)
-    check(lib().moe_dispatch_backward(dxs.data_ptr(), dt, rows, T, k, H, _ld(fn, "dxs", dxs, rows, H), inv.data_ptr(),
-                                      out.data_ptr(), _ld(fn, "out", out, T, H), _raw_stream(dev)))
+    status = lib().moe_dispatch_backward(dxs.data_ptr(), dt, rows, T, k, H, _ld(fn, "dxs", dxs, rows, H), inv.data_ptr(),
+                                      out.data_ptr(), _ld(fn, "out", out, T, H), _raw_stream(dev))
+    if status:
+        check(status)
     return out
 
 
@@ -342,9 +356,11 @@ def combine(ys, inv, gates=None, out_dtype=None, out=None, stream=None):
     rows, H = _two(fn, "ys", ys)
     T, k = _pairs(fn, inv, None, dev, gates)
     out = _new(T, H, out_dtype or ys.dtype) if out is None else _out(fn, out, out_dtype, T, H, dev)
-    check(lib().moe_combine(ys.data_ptr(), _float(fn, "ys", ys), rows, T, k, H, _ld(fn, "ys", ys, rows, H),
+    status = lib().moe_combine(ys.data_ptr(), _float(fn, "ys", ys), rows, T, k, H, _ld(fn, "ys", ys, rows, H),
                             inv.data_ptr(), None if gates is None else gates.data_ptr(), out.data_ptr(),
-                            _float(fn, "out", out), _ld(fn, "out", out, T, H), _raw_stream(dev)))
+                            _float(fn, "out", out), _ld(fn, "out", out, T, H), _raw_stream(dev))
+    if status:
+        check(status)
     return out
 
 
@@ -364,8 +380,10 @@ def combine_backward(dy, ys, inv, gates=None, out=None, stream=None):
     k = _pairs(fn, inv, T, dev, gates)[1]
     out = _new(rows, H, ys.dtype) if out is None else _out(fn, out, ys.dtype, rows, H, dev)
     dgates = _new(T, k, _F32)
-    check(lib().moe_combine_backward(dy.data_ptr(), _float(fn, "dy", dy), _ld(fn, "dy", dy, T, H), ys.data_ptr(),
+    status = lib().moe_combine_backward(dy.data_ptr(), _float(fn, "dy", dy), _ld(fn, "dy", dy, T, H), ys.data_ptr(),
                                      _float(fn, "ys", ys), _ld(fn, "ys", ys, rows, H), rows, T, k, H, inv.data_ptr(),
                                      None if gates is None else gates.data_ptr(), out.data_ptr(),
-                                     _ld(fn, "out", out, rows, H), dgates.data_ptr(), _raw_stream(dev)))
+                                     _ld(fn, "out", out, rows, H), dgates.data_ptr(), _raw_stream(dev))
+    if status:
+        check(status)
     return out, dgates
