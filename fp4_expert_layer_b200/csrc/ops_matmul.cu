@@ -35,7 +35,7 @@ namespace {
 
 constexpr int kMmThreads = 320;
 
-template <int WF, int NT>
+template <int WF, int NT, bool SPLIT>
 struct MmGeom {
   static constexpr int NBLK = (WF == WF_MX) ? 2 : 4;       // 4-scale blocks of 256 K
   static constexpr int SF_BYTES = NBLK * 512;
@@ -43,21 +43,25 @@ struct MmGeom {
   static constexpr int B_BYTES = NT * 128;
   static constexpr int SF_OFF = A_BYTES + B_BYTES;
   static constexpr int STAGE = (SF_OFF + 2 * SF_BYTES + 1023) / 1024 * 1024;
-  static constexpr int FIT = (205 * 1024) / STAGE;
+  static constexpr int RECV = SPLIT ? 128 * NT * 4 : 0;    // the cluster's parts, beside the stages
+  static constexpr int FIT = (205 * 1024 - RECV) / STAGE;
   static constexpr int NBUF = 2;
   static constexpr int SF_COLS = 2 * NBLK * 4;             // TMEM columns a stage's scales take
   static constexpr int SF_TMEM = NBUF * NT;
   static constexpr int SF_FIT = (512 - SF_TMEM) / SF_COLS;
   static constexpr int STAGES = FIT < 8 ? (FIT < SF_FIT ? FIT : SF_FIT) : (8 < SF_FIT ? 8 : SF_FIT);
-  static constexpr size_t SMEM = (size_t)STAGES * STAGE + 1024;
+  static constexpr size_t SMEM = (size_t)STAGES * STAGE + RECV + 1024;
   static_assert(STAGES >= 3, "a pipeline");
   static_assert(SF_TMEM + STAGES * SF_COLS <= 512, "TMEM budget");
   static_assert(SMEM + 17 * 1024 <= 227 * 1024, "shared-memory budget");
 };
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
 template <int WF, int NT, bool SPLIT>
 __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_constant__ MatmulArgs a) {
-  using Geo = MmGeom<WF, NT>;
+  using Geo = MmGeom<WF, NT, SPLIT>;
   constexpr int S = Geo::STAGES, NBUF = Geo::NBUF, WORDS = kSfWords<WF>;
   extern __shared__ __align__(1024) uint8_t mm_raw[];
   __shared__ __align__(8) uint64_t full_bar[S];
@@ -67,22 +71,23 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
   __shared__ __align__(8) uint64_t quiesce_bar;
   __shared__ uint32_t tmem_base_s;
   __shared__ MmGroups groups;
-  __shared__ int ok_s;
 
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(mm_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  if (tid == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(smem_u32(&full_bar[s]), 3);                // the codes' copies and two scale warps
-      mbar_init(smem_u32(&empty_bar[s]), 1);
-    }
+  if (tid < S) {
+    mbar_init(smem_u32(&full_bar[tid]), 3);                // the codes' copies and two scale warps
+    mbar_init(smem_u32(&empty_bar[tid]), 1);
+    mbar_fence_init();
+  }
+  if (tid == 32 * 2) {
+    tmap_prefetch(&a.wmap);
+    tmap_prefetch(&a.xmap);
     for (int b = 0; b < NBUF; ++b) {
       mbar_init(smem_u32(&accf_bar[b]), 1);
       mbar_init(smem_u32(&acce_bar[b]), 4);
     }
     mbar_init(smem_u32(&quiesce_bar), 1);
-    ok_s = 1;
     mbar_fence_init();
   }
   if (warp == 1) {
@@ -95,6 +100,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base_s;
+  if constexpr (SPLIT) cluster_arrive();                   // this CTA's shared memory may be written from now on
   const int nrb = (a.N + 127) / 128;
   const int nk_all = (a.K + 255) / 256;
 
@@ -105,8 +111,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
     rank = (int)cg::this_cluster().block_rank();
   }
   const int k0 = nk_all * rank / ranks, k1 = nk_all * (rank + 1) / ranks;
-  const long long first = SPLIT ? blockIdx.x / ranks : blockIdx.x;
-  const long long step = SPLIT ? (long long)(groups.tiles[a.groups] + 1) * nrb : gridDim.x;   // split: one item at most
+  const unsigned first = SPLIT ? blockIdx.x / (unsigned)ranks : blockIdx.x, step = SPLIT ? 0u : gridDim.x;
   using Walk = MmWalk<NT>;
 
   if (warp == 0) {
@@ -186,7 +191,6 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
     if (elect_one()) tc_commit(smem_u32(&quiesce_bar));
     __syncwarp();
     mbar_drain(smem_u32(&quiesce_bar), 0);
-    if (failed && lane == 0) ok_s = 0;
   } else if (warp < 6) {
     // ---------------- accumulators to y: warp w has TMEM lanes 32 * (w % 4) ..
     if constexpr (!SPLIT) {
@@ -225,7 +229,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
     constexpr int RG = (NT + 31) / 32 < 4 ? (NT + 31) / 32 : 4;        // 32-row groups of a token tile
     const uint8_t *rowp[4];
     const uint32_t off = Geo::SF_OFF + (tokens ? Geo::SF_BYTES : 0) + 16 * lane;
-    feed_scales<WF, S>(
+    feed_scales<WF, S, true>(
         a, groups, Walk(a, groups, nrb, first, step), k0, k1, (warp - 6) >> 1, 2,
         [&](const Walk &m) {
 #pragma unroll
@@ -242,31 +246,28 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
             for (int b = 0; b < WORDS; ++b)                // rows past the tile's: any number, their columns go nowhere
               sts128(dst + 512 * b, make_uint4(w[0][i * WORDS + b], w[1][i * WORDS + b], w[2][i * WORDS + b],
                                                w[3][i * WORDS + b]));
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&full_bar[s]));
           };
+        },
+        [&](int s) {
+          if (lane == 0) mbar_arrive(smem_u32(&full_bar[s]));
         });
   }
 
   if constexpr (SPLIT) {
     // parts meet: rank q finishes weight rows [128 q / ranks, 128 (q + 1) / ranks)
     cg::cluster_group cluster = cg::this_cluster();
-    float *recv = reinterpret_cast<float *>(smem);         // [source][rows of a rank][NT], over the stages
+    float *recv = reinterpret_cast<float *>(smem + (size_t)S * Geo::STAGE);   // [source][rows of a rank][NT]
     const Walk m(a, groups, nrb, first, step);
     const bool any = m.more();                             // the same for the whole cluster
-    if (any && warp >= 2 && warp < 6) {
-      if (!mbar_wait_warp(smem_u32(&accf_bar[0]), 0, a.err, 66) && lane == 0) ok_s = 0;
-    }
+    bool ok = k1 > k0;                                     // a rank without stages adds nothing
+    if (any && warp >= 2 && warp < 6) ok = mbar_wait_warp(smem_u32(&accf_bar[0]), 0, a.err, 66) && ok;
     __syncwarp();
-    tc_fence_before();
-    cluster.sync();                                        // every rank is done with its stages
+    cluster_wait();                                        // every rank has begun (long ago)
     const int per = 128 / ranks;                           // ranks is a power of two
     if (any && warp >= 2 && warp < 6) {
       tc_fence_after();
       const int quad = warp & 3, row = 32 * quad + lane;
       float *dst = cluster.map_shared_rank(recv, row / per) + ((size_t)rank * per + row % per) * NT;
-      const bool ok = ok_s != 0 && k1 > k0;                // a rank without stages adds nothing
 #pragma unroll 1
       for (int c0 = 0; c0 < NT; c0 += 16) {
         uint32_t v[16];
@@ -344,7 +345,7 @@ moe_status_t matmul_error_word(const char *fn, ErrWord **out) {
 
 template <int WF, int NT, bool SPLIT>
 cudaError_t launch_matmul(const MatmulArgs &a, int grid, int ranks, cudaStream_t s) {
-  using Geo = MmGeom<WF, NT>;
+  using Geo = MmGeom<WF, NT, SPLIT>;
   auto fn = fp4_matmul_kernel<WF, NT, SPLIT>;
   static std::atomic<uint64_t> asked{0};
   const cudaError_t e = ask_shared(fn, Geo::SMEM, asked);

@@ -42,12 +42,21 @@ struct MmGroups {
 template <int NT>
 __device__ __forceinline__ void mm_scan_groups(const MatmulArgs &a, MmGroups &t) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = blockDim.x;
+  if (!a.offsets) {                                        // one group of all rows: no scan
+    if (tid == 0) {
+      t.begin[0] = 0;
+      t.end[0] = a.rows;
+      t.tiles[0] = 0;
+      t.tiles[1] = (a.rows + NT - 1) / NT;
+    }
+    return;
+  }
   const int per = (a.groups + n - 1) / n;
   const int g0 = min(a.groups, tid * per), g1 = min(a.groups, g0 + per);
   int sum = 0;
   for (int g = g0; g < g1; ++g) {
-    const int b = a.offsets ? min(max(__ldg(a.offsets + g), 0), a.rows) : 0;
-    const int e = a.offsets ? min(max(__ldg(a.offsets + g + 1), 0), a.rows) : a.rows;
+    const int b = min(max(__ldg(a.offsets + g), 0), a.rows);
+    const int e = min(max(__ldg(a.offsets + g + 1), 0), a.rows);
     t.begin[g] = b;
     t.end[g] = max(b, e);
     t.tiles[g] = sum;
@@ -61,13 +70,16 @@ __device__ __forceinline__ void mm_scan_groups(const MatmulArgs &a, MmGroups &t)
   }
   if (lane == 31) t.wsum[warp] = inc;
   __syncthreads();
-  int earlier = inc - sum, all = 0;
-  for (int w = 0; w < n / 32; ++w) {
-    if (w < warp) earlier += t.wsum[w];
-    all += t.wsum[w];
+  int through = lane < n / 32 ? t.wsum[lane] : 0;          // every warp scans the warps' sums for itself
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, through, o);
+    if (lane >= o) through += v;
   }
+  const int prior = __shfl_sync(0xffffffffu, through, (warp + 31) & 31);
+  const int earlier = (warp ? prior : 0) + inc - sum;
   for (int g = g0; g < g1; ++g) t.tiles[g] += earlier;
-  if (tid == 0) t.tiles[a.groups] = all;
+  if (tid == n - 1) t.tiles[a.groups] = earlier + sum;
 }
 
 // A warp's walk over the items first, first + step, ...: item = tile * nrb + row
@@ -77,12 +89,13 @@ template <int NT>
 struct MmWalk {
   int g, row0, nrows, rb;        // of the item: group, first row, rows, block of weight rows
   int tile, dtile, drb, nrb, ntiles;
-  __device__ __forceinline__ MmWalk(const MatmulArgs &a, const MmGroups &t, int nrb_, long long first, long long step)
+  // step 0: the first item alone
+  __device__ __forceinline__ MmWalk(const MatmulArgs &a, const MmGroups &t, int nrb_, unsigned first, unsigned step)
       : g(0), nrb(nrb_), ntiles(t.tiles[a.groups]) {
-    tile = (int)(first / nrb);
-    rb = (int)(first - (long long)tile * nrb);
-    dtile = (int)(step / nrb);
-    drb = (int)(step - (long long)dtile * nrb);
+    tile = (int)(first / (unsigned)nrb);
+    rb = (int)(first - (unsigned)(tile * nrb));
+    dtile = step ? (int)(step / (unsigned)nrb) : ntiles;
+    drb = step ? (int)(step - (unsigned)(dtile * nrb)) : 0;
     find(a, t);
   }
   __device__ __forceinline__ bool more() const { return tile < ntiles; }
@@ -171,11 +184,16 @@ __device__ __forceinline__ void fetch_sf(const MatmulArgs &a, const uint8_t *con
 
 // A scale warp's work: of the sequence (item, steps of AHEAD stages in [k0, k1)) it
 // takes every `stride`-th step from `phase` on, loads the next of them while it
-// stores the last.  rows_of(walk) sets the row pointers of an item; put(s, stage's
-// words, i) stores one stage's blocks into ring place s and arrives.
-template <int WF, int S, typename Walk, typename RowsOf, typename Fetch, typename Wait, typename Put>
+// stores the last.  rows_of(walk) sets the row pointers of an item; put(walk) gives
+// the function that stores stage i of a step of that item into ring place s.
+// A step's stages are stored one by one, or (BATCH) all before the one fence that
+// shows them to the tensor core, which costs some 500 clocks: with a ring of two
+// steps and more the copies lose nothing by it.
+template <int WF, int S, bool BATCH, typename Walk, typename RowsOf, typename Fetch, typename Wait, typename Put,
+          typename Arrive>
 __device__ __forceinline__ void feed_scales(const MatmulArgs &a, const MmGroups &t, Walk m, int k0, int k1, int phase,
-                                            int stride, RowsOf rows_of, Fetch fetch, Wait wait_empty, Put put) {
+                                            int stride, RowsOf rows_of, Fetch fetch, Wait wait_empty, Put put,
+                                            Arrive arrive) {
   constexpr int AHEAD = kSfAhead<WF>;
   int it0 = k0, seq = 0;                                   // seq: stages before this step, over all items
   bool more = m.more() && k1 > k0;
@@ -208,7 +226,15 @@ __device__ __forceinline__ void feed_scales(const MatmulArgs &a, const MmGroups 
       const int s = (first + i) % S, round = (first + i) / S;
       if (round > 0 && !wait_empty(s, (round - 1) & 1)) return;
       ticket(s, hold, i);
+      if (BATCH) continue;
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      arrive(s);
     }
+    if (!BATCH) continue;
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    for (int i = 0; i < stages; ++i) arrive((first + i) % S);
   }
 }
 

@@ -69,11 +69,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(pm_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  if (tid == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(smem_u32(&full_bar[s]), 1 + 2 * 3);        // the copies' bytes, three scale warps of each CTA
-      mbar_init(smem_u32(&empty_bar[s]), 1);
-    }
+  if (tid < S) {
+    mbar_init(smem_u32(&full_bar[tid]), 1 + 2 * 3);        // the copies' bytes, three scale warps of each CTA
+    mbar_init(smem_u32(&empty_bar[tid]), 1);
+    mbar_fence_init();
+  }
+  if (tid == 32 * 2) {
+    tmap_prefetch(&a.wmap);
+    tmap_prefetch(&a.xmap);
     mbar_init(smem_u32(&accf_bar[0]), 1);
     mbar_init(smem_u32(&accf_bar[1]), 1);
     mbar_init(smem_u32(&free_bar), 2 * kPairEpi);
@@ -93,7 +96,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
   const uint32_t tmem = tmem_base_s;
   const int nrb = (a.N + 255) / 256;
   const int nk = (a.K + 255) / 256;
-  const long long first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const unsigned first = blockIdx.x >> 1, step = gridDim.x >> 1;
   using Walk = MmWalk<kPairRows>;
 
   if (warp == 0) {
@@ -280,7 +283,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
     const int pitch = which == 0 ? 512 : 1024;             // between a stage's blocks
     const uint8_t *rowp[4];
     bool wanted = false;                                   // the second half of a narrow tile is not read
-    feed_scales<WF, S>(
+    feed_scales<WF, S, false>(
         a, groups, Walk(a, groups, nrb, first, step), 0, nk, 0, 1,
         [&](const Walk &m) {
           wanted = which < 2 || m.nrows > 128;
@@ -294,17 +297,16 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
         [&](int s, uint32_t parity) { return mbar_wait_warp(smem_u32(&empty_bar[s]), parity, a.err, 75); },
         [&](const Walk &) {
           return [&, store = wanted](int s, const uint32_t(&w)[4][8], int i) {
-            if (store) {
-              const uint32_t dst = smem_u32(smem + (size_t)s * Geo::STAGE) + off;
+            if (!store) return;
+            const uint32_t dst = smem_u32(smem + (size_t)s * Geo::STAGE) + off;
 #pragma unroll
-              for (int b = 0; b < WORDS; ++b)
-                sts128(dst + pitch * b, make_uint4(w[0][i * WORDS + b], w[1][i * WORDS + b], w[2][i * WORDS + b],
-                                                   w[3][i * WORDS + b]));
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-              __syncwarp();
-            }
-            if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&full_bar[s]), 0));
+            for (int b = 0; b < WORDS; ++b)
+              sts128(dst + pitch * b, make_uint4(w[0][i * WORDS + b], w[1][i * WORDS + b], w[2][i * WORDS + b],
+                                                 w[3][i * WORDS + b]));
           };
+        },
+        [&](int s) {
+          if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&full_bar[s]), 0));
         });
   }
 
