@@ -367,20 +367,6 @@ cudaError_t launch_matmul(const MatmulArgs &a, int grid, int ranks, cudaStream_t
   return cudaLaunchKernelEx(&cfg, fn, a);
 }
 
-template <int WF>
-cudaError_t run_matmul(const MatmulArgs &a, int nt, int grid, int ranks, cudaStream_t s) {
-  if (ranks > 1) {
-    if (nt == 16) return launch_matmul<WF, 16, true>(a, grid, ranks, s);
-    if (nt == 32) return launch_matmul<WF, 32, true>(a, grid, ranks, s);
-    if (nt == 64) return launch_matmul<WF, 64, true>(a, grid, ranks, s);
-    return launch_matmul<WF, 128, true>(a, grid, ranks, s);
-  }
-  if (nt == 16) return launch_matmul<WF, 16, false>(a, grid, 1, s);
-  if (nt == 32) return launch_matmul<WF, 32, false>(a, grid, 1, s);
-  if (nt == 64) return launch_matmul<WF, 64, false>(a, grid, 1, s);
-  return launch_matmul<WF, 128, false>(a, grid, 1, s);
-}
-
 }  // namespace
 }  // namespace moe
 
@@ -410,19 +396,28 @@ extern "C" moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_
   MatmulArgs a{};
   auto enc = map_encoder();
   if (!enc) return ops_fail(MOE_ERR_CUDA, fn, "cuTensorMapEncodeTiled is unavailable");
-  // rows a group can be expected to have decide the token tile: the least tile
-  // that holds them, so that a decode batch streams weights and little else
-  const int64_t mean = (rows + n_groups - 1) / n_groups;
-  const int nt = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 128;
+  // Which kernel, by the rows a group has on average and the blocks of 128 weight
+  // rows that can be in use (graph-timed us, N = K = 2048, NVFP4, unless said):
+  //  * up to 32 rows and blocks for every SM: weights are streamed, one CTA a block
+  //    with token tiles of 32 (64 groups: 29.9 at 8 rows a group and 31.2 at 20;
+  //    pairs 35.3 and 36.0; 38.0 and 37.7 at 40);
+  //  * up to 16 rows and fewer blocks: K split over clusters, tiles of 16 (dense, 1
+  //    row, N 4096: 5.7; unsplit 6.8, tiles of 32 6.3, pairs 7.0);
+  //  * else pairs (dense, 64 rows, N 4096: 7.9, one CTA a block 10.2; 128 rows a
+  //    group, 64 groups: 46; 92).
   const int sms = sm_count();
-  // CTA pairs where the rows fill a wide tile and there are items for every pair
-  const int64_t pair_items = (rows / kPairRows + n_groups) * (int64_t)((N + 255) / 256);
-  const bool pairs = mean > 64 && pair_items >= sms / 2;
+  const int64_t mean = (rows + n_groups - 1) / n_groups, blocks = std::min<int64_t>(n_groups, rows) * ((N + 127) / 128);
+  // tiles there can be at most (without offsets: there are)
+  auto tiles = [&](int64_t nt) {
+    return offsets ? std::min<int64_t>(rows, rows / nt + n_groups) : (rows + nt - 1) / nt;
+  };
+  const bool streamed = mean <= 32 && blocks >= sms, split = !streamed && mean <= 16;
+  const int nt = streamed ? 32 : split ? 16 : kPairRows;
   const cuuint64_t kb = (cuuint64_t)(K / 2);
   const cuuint32_t ones[3] = {1, 1, 1};
   {
     const cuuint64_t dims[2] = {kb, (cuuint64_t)rows}, strides[1] = {kb};
-    const cuuint32_t box[2] = {128, (cuuint32_t)(pairs ? kPairBox : nt)};
+    const cuuint32_t box[2] = {128, (cuuint32_t)(nt == kPairRows ? kPairBox : nt)};
     if (enc(&a.xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(x_codes), dims, strides, box, ones,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -458,19 +453,22 @@ extern "C" moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_
   a.sf_wide = a.sf_mode == 0 && a.nsf % 16 == 0 && aligned_to(x_scales, 16) && aligned_to(w_scales, 16);
   a.y_vec = row_alignment(y, ldy * dtype_bytes(dtype)) >= 16;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (pairs)
-    return ops_launched(fn, launch_matmul_pair(fmt == MOE_FMT_MXFP4 ? WF_MX : WF_NV, a,
-                                               (int)std::min<int64_t>(pair_items, sms / 2), s));
-  // items there can be at most, and the ways to split K when they leave SMs idle:
-  // each way keeps at least two stages
-  const int64_t nrb = (N + 127) / 128;
-  const int64_t tiles = std::min<int64_t>(rows, rows / nt + n_groups);
-  const int64_t items = tiles * nrb;
-  const int nk = (K + 255) / 256;
-  int ranks = 1;
-  while (ranks < 8 && items * ranks * 2 <= sms && nk >= 4 * ranks) ranks *= 2;
-  const int grid = (int)std::min<int64_t>(items, ranks > 1 ? items : sms);
-  const cudaError_t e = fmt == MOE_FMT_MXFP4 ? run_matmul<WF_MX>(a, nt, grid, ranks, s)
-                                             : run_matmul<WF_NV>(a, nt, grid, ranks, s);
+  const bool mx = fmt == MOE_FMT_MXFP4;
+  cudaError_t e;
+  if (streamed) {
+    const int grid = (int)std::min<int64_t>(tiles(32) * ((N + 127) / 128), sms);
+    e = mx ? launch_matmul<WF_MX, 32, false>(a, grid, 1, s) : launch_matmul<WF_NV, 32, false>(a, grid, 1, s);
+  } else if (split) {
+    // one item a cluster; as many ways as keep every cluster resident (a second
+    // round doubles the time) and leave each way two stages
+    const int64_t items = tiles(16) * ((N + 127) / 128);
+    const int nk = (K + 255) / 256;
+    int ranks = 1;
+    while (ranks < 8 && items * ranks * 2 <= sms && nk >= 4 * ranks) ranks *= 2;
+    e = mx ? launch_matmul<WF_MX, 16, true>(a, (int)items, ranks, s) : launch_matmul<WF_NV, 16, true>(a, (int)items, ranks, s);
+  } else {
+    const int pairs = (int)std::min<int64_t>(tiles(kPairRows) * ((N + 255) / 256), sms / 2);
+    e = launch_matmul_pair(mx ? WF_MX : WF_NV, a, pairs, s);
+  }
   return ops_launched(fn, e);
 }

@@ -391,7 +391,7 @@ def test_dense_product(fmt, rows, N, K):
 GROUPED = [  # segment lengths, rows behind, N, K
     ([1], 0, 64, 64), ([0, 1, 0], 2, 128, 256), ([3, 0, 17, 16, 0, 1], 0, 200, 512), ([40, 5, 130, 0, 64], 3, 256, 288),
     ([256, 1, 129, 300], 0, 129, 1024), ([0, 0], 5, 128, 64), ([2] * 64, 0, 512, 2048), ([1] * 100 + [0] * 24, 1, 130, 96),
-    ([0] * 1000 + [7] + [0] * 23, 0, 128, 128), ([700], 9, 320, 256),
+    ([0] * 1000 + [7] + [0] * 23, 0, 128, 128), ([700], 9, 320, 256), ([20, 45, 0, 31, 40, 33] * 10, 2, 400, 288),
 ]
 
 
