@@ -259,8 +259,8 @@ cudaError_t launch_combine_bwd(CombineBwdArgs a, bool vec, cudaStream_t s) {
 
 // ------------------------------------------------------------ argument checks
 moe_status_t check_shape(const char *fn, int32_t T, int32_t k, int32_t H, int32_t rows) {
-  if (T < 0 || k < 1 || k > kMaxTopK || H < 1 || rows < 0)
-    return ops_invalid(fn, "need T >= 0, 1 <= k <= 32, H >= 1 and rows >= 0");
+  if (T < 0 || k < 1 || k > kMaxTopK || H < 1 || H > 1 << 28 || rows < 0)
+    return ops_invalid(fn, "need T >= 0, 1 <= k <= 32, 1 <= H <= 2^28 and rows >= 0");
   if ((int64_t)T * k >= (int64_t)1 << 31) return ops_invalid(fn, "T * k must be below 2^31");
   return MOE_OK;
 }

@@ -74,9 +74,13 @@ moe_status_t moe_fp4_dequantize(const uint8_t *codes, const uint8_t *scales, con
  * them); NULL: n_groups = 1 and every row is in it.  Rows of y before offsets[0]
  * or behind offsets[n_groups] are left as they were.  Sums do not depend on the
  * order in which the GPU runs them: equal calls give equal bits.
+ * Scale codes are read as in moe_admit: a NaN code makes its block NaN, NVFP4
+ * scales must not be negative.
  * K is a multiple of 32, 1 <= n_groups <= 1024; codes are 16-byte aligned and y
  * aligned to its type; rows <= 2^27; N, K and n_groups * N below 2^31.  The scale rows
- * are read fastest when K is a multiple of 256 and they are 16-byte aligned. */
+ * are read fastest when they start on 16 bytes (K a multiple of 512, with NVFP4 of
+ * 256).  Every wait inside the kernel is bounded: should one give up, that call's y
+ * is invalid and the next call on the device returns MOE_ERR_CUDA, once. */
 moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_scales, const float *x_global, int32_t rows,
                             const uint8_t *w_codes, const uint8_t *w_scales, const float *w_global, int32_t n_groups,
                             int32_t N, int32_t K, int32_t fmt, const int32_t *offsets, void *y, int32_t dtype,
@@ -94,7 +98,8 @@ moe_status_t moe_sort_tokens(const int32_t *ids, int32_t T, int32_t k, int32_t E
 /* Send each token's row to its pairs: xs[inv[t * k + j]] = x[t] for every pair
  * with inv in [0, rows).  x [T, H], xs [rows, H], any element type.  Rows of xs
  * that no pair names are left as they were.  The positions in inv must differ
- * from one another (moe_sort_tokens writes such an inv). */
+ * from one another (moe_sort_tokens writes such an inv).  1 <= k <= 32,
+ * 1 <= H <= 2^28 and T * k < 2^31 here and in the three calls below. */
 moe_status_t moe_dispatch(const void *x, int32_t dtype, int32_t T, int32_t k, int32_t H, int64_t ldx,
                           const int32_t *inv, int32_t rows, void *xs, int64_t ldxs, void *stream);
 

@@ -555,6 +555,84 @@ def test_graph_replays_the_path_and_streams_do_not_mix(fmt):
         assert t.equal(y, F.combine(F.dispatch(a, r["inv"]), r["inv"], gt))
 
 
+def test_wide_products_on_two_streams_at_once():
+    """Two products that each fill the GPU, in flight together, many times over."""
+    t, F = G.torch(), G.library()
+    E, N, K = 8, 1536, 1024
+    work = []
+    for i in range(2):
+        x, w = _operands("nvfp4", 1500, E, N, K, 90 + i)
+        off = t.tensor(np.linspace(0, 1500, E + 1).astype(np.int32), device="cuda")
+        work.append((x, w, off, F.fp4_matmul(x, w, off)))
+    streams = [t.cuda.Stream(), t.cuda.Stream()]
+    t.cuda.synchronize()
+    got = [[F.fp4_matmul(x, w, off, stream=s) for s, (x, w, off, _) in zip(streams, work)] for _ in range(20)]
+    t.cuda.synchronize()
+    for pair in got:
+        for y, (_, _, _, want) in zip(pair, work):
+            assert t.equal(y, want)
+
+
+FIRST_CALL = r"""
+import torch as t
+import fp4_expert_layer_b200 as F
+x = t.randn(40, 256, device="cuda").bfloat16()
+w = t.randn(64, 256, device="cuda").bfloat16()
+ids = t.randint(0, 4, (40, 2), dtype=t.int32, device="cuda")
+def path():
+    r = F.sort_tokens(ids, 4)
+    y = F.fp4_matmul(F.fp4_quantize(x, "nvfp4"), F.fp4_quantize(w, "nvfp4", rows_per_scale=64))
+    xs = F.dispatch(y, r["inv"])
+    return F.combine(xs, r["inv"])
+g = t.cuda.CUDAGraph()
+with t.cuda.graph(g):
+    got = path()
+g.replay()
+t.cuda.synchronize()
+assert t.equal(got, path()) and t.isfinite(got).all() and got.abs().max() > 0
+print("first call captured")
+"""
+
+
+def test_first_call_of_a_process_may_be_captured():
+    import os
+    import subprocess
+    import sys
+    G.library()
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], capture_output=True, text=True, timeout=600,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "first call captured" in r.stdout, r.stdout[-1000:] + r.stderr[-3000:]
+
+
+def test_more_than_2_31_elements():
+    """Element offsets that pass 32 bits: the last rows against calls on those rows alone."""
+    t, F = G.torch(), G.library()
+    T, H, tail = 270_000, 8192, 300                        # 2.2e9 elements, 4.4 GB in bf16
+    x = t.randn((T, H), device="cuda", dtype=t.bfloat16)
+    inv = t.arange(T - 1, -1, -1, dtype=t.int32, device="cuda").view(T, 1)
+    xs = F.dispatch(x, inv)
+    assert t.equal(xs[:tail], x[-tail:].flip(0)) and t.equal(xs[-tail:], x[:tail].flip(0))
+    back = F.combine(xs, inv, t.full((T, 1), 2.0, device="cuda"))
+    assert t.equal(back[-tail:], 2 * x[-tail:]) and t.equal(back[:tail], 2 * x[:tail])
+    dys, dg = F.combine_backward(x, back, inv, out=xs)
+    assert t.equal(dys[:tail], x[-tail:].flip(0))
+    term = x[-tail:].double() * back[:tail].flip(0).double()
+    off = dg[-tail:, 0].double() - term.sum(1)
+    assert bool((off.abs() <= H * 2.0 ** -24 * term.abs().sum(1)).all())
+    del back, dys, xs
+    for fmt in ("mxfp4", "nvfp4"):
+        q, last = F.fp4_quantize(x, fmt), F.fp4_quantize(x[-tail:], fmt)
+        assert all(a is None or t.equal(a[-tail:], b) for a, b in zip(q[:3], last[:3]))
+        assert t.equal(F.fp4_dequantize(q, dtype=t.bfloat16)[-tail:], F.fp4_dequantize(last, dtype=t.bfloat16))
+    one = F.fp4_quantize(x, "nvfp4", rows_per_scale=T)
+    assert t.equal(one.global_scale[0], q.global_scale.max())
+    del x, q, last, one
+    x, w = _operands("mxfp4", 550_000, 1, 4104, 32, 95)
+    y = F.fp4_matmul(x, w)
+    last = F.FP4Tensor(x.codes[-tail:].clone(), x.scales[-tail:].clone(), None, "mxfp4")
+    assert t.equal(y[-tail:], F.fp4_matmul(last, w))
+
+
 def test_backward_in_a_graph():
     t, F = G.torch(), G.library()
     T, k, E, H = 40, 3, 8, 136

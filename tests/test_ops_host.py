@@ -46,7 +46,7 @@ MATMUL = dict(xc=P, xs=P, xG=P, rows=4, wc=P, ws=P, wG=P, groups=2, N=8, K=64, f
 
 
 @pytest.mark.parametrize("bad", [
-    dict(rows=-1), dict(groups=0), dict(groups=1025), dict(N=0), dict(K=0), dict(K=40), dict(fmt=3), dict(dtype=3),
+    dict(rows=-1), dict(rows=(1 << 27) + 1), dict(groups=0), dict(groups=1025), dict(N=0), dict(K=0), dict(K=40), dict(fmt=3), dict(dtype=3),
     dict(ldy=7), dict(xc=None), dict(xs=None), dict(wc=None), dict(ws=None), dict(y=None), dict(xG=None),
     dict(wG=None), dict(offsets=None), dict(xc=C.c_void_p(4104)), dict(wc=C.c_void_p(4104)), dict(y=C.c_void_p(4097)),
     dict(offsets=C.c_void_p(4098)), dict(groups=1024, N=1 << 21, ldy=1 << 21),
@@ -77,7 +77,8 @@ CBWD = dict(dy=P, ddy=1, lddy=8, ys=P, dys_t=1, ldys=8, rows=8, T=4, k=2, H=8, i
 
 @pytest.mark.parametrize("fn, base, bad", [
     ("moe_dispatch", DISPATCH, b) for b in (
-        dict(dtype=4), dict(T=-1), dict(k=0), dict(k=33), dict(H=0), dict(rows=-1), dict(ldx=7), dict(ldxs=7),
+        dict(dtype=4), dict(T=-1), dict(k=0), dict(k=33), dict(H=0), dict(H=(1 << 28) + 1, ldx=1 << 30, ldxs=1 << 30),
+        dict(rows=-1), dict(ldx=7), dict(ldxs=7),
         dict(x=None), dict(inv=None), dict(xs=None), dict(x=C.c_void_p(4097)), dict(T=1 << 30, k=2))
 ] + [
     ("moe_dispatch_backward", DBWD, b) for b in (
