@@ -19,7 +19,13 @@
 //    multiple of 2^-16 (|v / d| <= 9), does in two operations.
 //
 // Bound by memory: x is read once and 0.53 or 0.56 bytes an element are written.
-// A thread takes 16 consecutive elements (one NVFP4 block, half an MXFP4 block).
+// A thread takes pieces of 16 consecutive elements (one NVFP4 block, half an MXFP4
+// block), 32 bytes of 16-bit elements in one access.  8192 x 4096 bf16: MXFP4 13.8
+// us quantised, 13.6 read back (94% and 95% of the copy rate); NVFP4 by rows 15.8
+// and 15.0 (83%, 88%): there the arithmetic, some 100 instructions a piece, shows.
+// An NVFP4 scale over many rows needs a pass over x before the codes: 64 matrices of
+// 1024 x 2048 98.3 us, of 93 for the two reads (a cluster a matrix, to read it again
+// from L2, takes 97 to 147).
 #include "ops_common.cuh"
 
 namespace moe {
@@ -165,9 +171,9 @@ struct FpArgs {
 // ------------------------------------------------------------------- quantise
 // A thread takes U pieces of 16 elements, flat over the rows, loads in flight
 // together.  MXFP4 halves meet by shuffle (K is a multiple of 32, so a block's
-// halves are neighbouring lanes); one piece a thread keeps HBM busy.  NVFP4 finds
-// its group's G in memory and does 1.5 times the work on a piece: with one piece a
-// thread its loads do not cover it (FLATU).
+// halves are neighbouring lanes); one piece a thread keeps HBM busy (65536 x 2048
+// bf16: 49.1 us, the copy rate).  NVFP4 finds its group's G in memory and takes two
+// (with the pass for G 98.3 us; with one 101.7, with four 100.4).
 template <typename T, int ALIGN, bool MX, int U>
 __global__ void __launch_bounds__(256) quantize_flat_kernel(const FpArgs a) {
   wait_prior_grid();
@@ -301,49 +307,47 @@ __global__ void __launch_bounds__(256) group_scale_kernel(const FpArgs a, uint32
 }
 
 // ----------------------------------------------------------------- dequantise
-template <typename T, int ALIGN, bool MX>
+template <typename T, int ALIGN, bool MX, int U>
 __global__ void __launch_bounds__(256) dequantize_kernel(const FpArgs a) {
   wait_prior_grid();
-  // four pieces a thread, their loads in flight together
-  const uint32_t i0 = blockIdx.x * 1024 + threadIdx.x;
-  uint2 code[4];
-  uint32_t scale[4], at[4];
-  float G[4];
+  // U pieces a thread, their loads in flight together
+  const uint32_t i0 = blockIdx.x * (256 * U) + threadIdx.x;
+  uint2 code[U];
+  uint32_t scale[U], row[U];
+  float G[U];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
+  for (int u = 0; u < U; ++u) {
     const uint32_t i = i0 + 256 * u;
     if (i >= a.total) break;
-    at[u] = a.by_cols.div(i);
+    row[u] = a.by_cols.div(i);
     code[u] = __ldg(reinterpret_cast<const uint2 *>(a.codes) + i);
     scale[u] = __ldg(a.scales + (MX ? i >> 1 : i));
-    G[u] = MX ? 1.0f : __ldg(a.G + a.by_group.div(at[u]));
+    G[u] = MX ? 1.0f : __ldg(a.G + a.by_group.div(row[u]));
   }
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-  const uint32_t i = i0 + 256 * u;
-  if (i >= a.total) break;
-  const uint32_t row = at[u], c = i - row * a.cols16;
-  const uint2 w = code[u];
-  float d;
-  if constexpr (MX) {
-    d = scale[u] == 255 ? __uint_as_float(0x7FC00000u)
-                        : scale[u] == 0 ? __uint_as_float(1u << 22) : __uint_as_float(scale[u] << 23);   // 0 is 2^-127
-  } else {
-    d = e4m3_any(scale[u]) * G[u];
-  }
-  Pack<T, 16, ALIGN> out;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t f[4];
-    e2m1x8_to_f16x2(h ? w.y : w.x, f);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 p = __half22float2(*reinterpret_cast<__half2 *>(&f[j]));
-      out.set(8 * h + 2 * j, p.x * d);
-      out.set(8 * h + 2 * j + 1, p.y * d);
+  for (int u = 0; u < U; ++u) {
+    const uint32_t i = i0 + 256 * u;
+    if (i >= a.total) break;
+    float d;
+    if constexpr (MX) {
+      d = scale[u] == 255 ? __uint_as_float(0x7FC00000u)
+                          : scale[u] == 0 ? __uint_as_float(1u << 22) : __uint_as_float(scale[u] << 23);   // 0 is 2^-127
+    } else {
+      d = e4m3_any(scale[u]) * G[u];
     }
-  }
-  out.store(static_cast<typename T::raw *>(const_cast<void *>(a.x)) + row * a.ldx + 16 * c);
+    Pack<T, 16, ALIGN> out;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t f[4];
+      e2m1x8_to_f16x2(h ? code[u].y : code[u].x, f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 p = __half22float2(*reinterpret_cast<__half2 *>(&f[j]));
+        out.set(8 * h + 2 * j, p.x * d);
+        out.set(8 * h + 2 * j + 1, p.y * d);
+      }
+    }
+    out.store(static_cast<typename T::raw *>(const_cast<void *>(a.x)) + row[u] * a.ldx + 16 * (i - row[u] * a.cols16));
   }
 }
 
@@ -404,20 +408,25 @@ cudaError_t quantize(const FpArgs &a, int32_t fmt, cudaStream_t s) {
                                 : quantize_rows_kernel<T, ALIGN, kMost>,
                      dim3((a.rows + rows_here - 1) / rows_here), tpr * rows_here, 0, s, a, tpr);
   }
-  constexpr uint32_t kFlat = sizeof(typename T::raw) == 4 ? 2 : 4;
   const uint32_t groups = a.rows / a.rows_per_scale, per_group = a.rows_per_scale * a.cols16;
   const uint32_t want = std::max<uint32_t>(1, (uint32_t)(8 * sm_count()) / groups);
   const uint32_t blocks = std::min<uint32_t>(want, (per_group + 1023) / 1024);   // four turns of a CTA at least
   cudaError_t e = cudaMemsetAsync(a.G, 0, (size_t)groups * sizeof(float), s);
   if (e == cudaSuccess) e = launch_op(group_scale_kernel<T, ALIGN>, dim3(groups * blocks), 256, 0, s, a, per_group, blocks);
-  if (e == cudaSuccess) e = launch_op(quantize_flat_kernel<T, ALIGN, false, kFlat>, flat_grid(a, kFlat), 256, 0, s, a);
+  if (e == cudaSuccess) e = launch_op(quantize_flat_kernel<T, ALIGN, false, 2>, flat_grid(a, 2), 256, 0, s, a);
   return e;
 }
 
 template <typename T, int ALIGN>
 cudaError_t dequantize(const FpArgs &a, int32_t fmt, cudaStream_t s) {
-  return launch_op(fmt == MOE_FMT_MXFP4 ? dequantize_kernel<T, ALIGN, true> : dequantize_kernel<T, ALIGN, false>,
-                   flat_grid(a, 4), 256, 0, s, a);
+  // one piece a thread until that fills the GPU, then four (MXFP4 to bf16, 8 x 2048:
+  // 1.2 us, with four 1.7; 8192 x 4096: 13.6, with one 14.6)
+  const bool mx = fmt == MOE_FMT_MXFP4;
+  if (a.total < (uint32_t)(sm_count() * 2048))
+    return launch_op(mx ? dequantize_kernel<T, ALIGN, true, 1> : dequantize_kernel<T, ALIGN, false, 1>, flat_grid(a, 1),
+                     256, 0, s, a);
+  return launch_op(mx ? dequantize_kernel<T, ALIGN, true, 4> : dequantize_kernel<T, ALIGN, false, 4>, flat_grid(a, 4),
+                   256, 0, s, a);
 }
 
 }  // namespace

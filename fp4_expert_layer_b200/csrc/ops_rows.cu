@@ -9,6 +9,11 @@
 // by token, not by sorted row, so that a token's row is read once for its k
 // pairs (dispatch and both gradients) and a sum over pairs stays in fp32
 // registers in ascending j: no atomics, one rounding, the same bits each time.
+//
+// Measured, bf16, 8192 tokens x 8 pairs, H 2048 (share of the copy rate): dispatch
+// 48.7 us (94%), its backward 51.2 (90%), combine 52.0 (89%), its backward 97.8
+// (89%); 33 tokens 2.2 to 4.2 us.  More rows in flight a warp (8, or wider columns)
+// cost registers and with them warps: 59 to 74 us for combine.
 #include "ops_common.cuh"
 
 namespace moe {

@@ -17,7 +17,8 @@
 // counts wait in inv, each in its own chunk's part, which that chunk's CTA reads
 // before it writes there, so there is no workspace either.
 //
-// Bound by latency: 12 bytes a pair are nothing next to the launches.
+// Bound by latency: 12 bytes a pair are nothing next to the launches.  264 pairs 2.8
+// us, 12K 7.0, 82K of 512 experts 8.1 (one cluster: 19), 524K 14 (81).
 #include <cooperative_groups.h>
 
 #include "ops_common.cuh"
