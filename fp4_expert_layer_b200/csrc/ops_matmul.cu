@@ -86,6 +86,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
     mbar_fence_init();
   }
   if (tid == 32 * 2) {
+    mm_set_mirror(a);
     tmap_prefetch(&a.wmap);
     tmap_prefetch(&a.xmap);
     for (int b = 0; b < NBUF; ++b) {
@@ -321,30 +322,41 @@ PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
   return fn;
 }
 
-// Error word of this device's products: mapped host memory, which the bounded
-// waits write to when they give up and the next call reads.  Made once per device.
-moe_status_t matmul_error_word(const char *fn, ErrWord **out) {
+// Error word of this device's products, in device memory (a poll of host memory
+// would put a PCIe round trip into a wait), and its mirror in mapped host memory,
+// which the next call reads.  Looked up and made once per device.
+__device__ ErrWord g_matmul_err;
+
+struct MatmulErr {
+  ErrWord *dev = nullptr;
+  int *host = nullptr;
+};
+
+moe_status_t matmul_error_word(const char *fn, MatmulErr *out) {
   static std::mutex mu;
-  static ErrWord *words[64] = {};
+  static MatmulErr words[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || dev < 0 || dev >= 64) return ops_fail(MOE_ERR_CUDA, fn, "no current device");
   std::lock_guard<std::mutex> lock(mu);
-  if (!words[dev]) {
-    // also inside a stream capture: pinned host memory takes no part in it
+  MatmulErr &w = words[dev];
+  if (!w.host) {
+    // also inside a stream capture: neither call takes part in it
     cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
     cudaThreadExchangeStreamCaptureMode(&mode);
-    void *p = nullptr;
-    e = cudaHostAlloc(&p, sizeof(ErrWord), cudaHostAllocMapped | cudaHostAllocPortable);
+    void *d = nullptr, *h = nullptr;
+    e = cudaGetSymbolAddress(&d, g_matmul_err);
+    if (e == cudaSuccess) e = cudaHostAlloc(&h, sizeof(int), cudaHostAllocMapped | cudaHostAllocPortable);
     cudaThreadExchangeStreamCaptureMode(&mode);
     if (e != cudaSuccess) {
       cudaGetLastError();
-      return ops_fail(MOE_ERR_OOM, fn, "no pinned host memory for the error word");
+      return ops_fail(MOE_ERR_CUDA, fn, std::string("no error word: ") + cudaGetErrorString(e));
     }
-    words[dev] = static_cast<ErrWord *>(p);
-    *words[dev] = ErrWord{0, 0, nullptr};
+    w.dev = static_cast<ErrWord *>(d);
+    w.host = static_cast<int *>(h);
+    *w.host = 0;
   }
-  *out = words[dev];
+  *out = w;
   return MOE_OK;
 }
 
@@ -436,18 +448,21 @@ extern "C" moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return ops_fail(MOE_ERR_CUDA, fn, "cuTensorMapEncodeTiled failed for w");
   }
-  ErrWord *err = nullptr;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  MatmulErr err;
   const moe_status_t st = matmul_error_word(fn, &err);
   if (st != MOE_OK) return st;
-  if (const int code = *(volatile int *)&err->code) {
-    *(volatile int *)&err->code = 0;
+  if (const int code = *(volatile int *)err.host) {
+    *(volatile int *)err.host = 0;
+    cudaMemsetAsync(&err.dev->code, 0, sizeof(int), s);
     return ops_fail(MOE_ERR_CUDA, fn, "a device-side wait of an earlier call gave up (code " + std::to_string(code) + ")");
   }
   a.xs = x_scales; a.ws = w_scales;
   a.xG = x_global; a.wG = w_global;
   a.offsets = offsets;
   a.y = y; a.ldy = ldy;
-  a.err = &err->code;
+  a.err = &err.dev->code;
+  a.err_host = err.host;
   a.rows = rows; a.groups = n_groups; a.N = N; a.K = K;
   a.nsf = K / (fmt == MOE_FMT_MXFP4 ? 32 : 16);
   a.dtype = dtype;
@@ -457,7 +472,6 @@ extern "C" moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_
                                                                                               : 2;
   a.sf_wide = a.sf_mode == 0 && a.nsf % 16 == 0 && aligned_to(x_scales, 16) && aligned_to(w_scales, 16);
   a.y_vec = row_alignment(y, ldy * dtype_bytes(dtype)) >= 16;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool mx = fmt == MOE_FMT_MXFP4;
   cudaError_t e;
   if (streamed) {

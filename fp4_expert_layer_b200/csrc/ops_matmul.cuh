@@ -20,7 +20,8 @@ struct MatmulArgs {
   const int *offsets;            // NULL: one group of all rows
   void *y;
   int64_t ldy;
-  int *err;
+  int *err;                      // the device's error word (an ErrWord), which the waits poll
+  int *err_host;                 // its mirror in mapped host memory
   int rows, groups, N, K;
   int nsf;                       // scales in a row
   int sf_mode;                   // 0: a stage's scales in one load, 1: words of four, 2: bytes
@@ -28,6 +29,11 @@ struct MatmulArgs {
   int dtype;
   int y_vec;                     // rows of y start on 16 bytes
 };
+
+// The error word knows its mirror; every CTA says so before it waits for anything.
+__device__ __forceinline__ void mm_set_mirror(const MatmulArgs &a) {
+  reinterpret_cast<ErrWord *>(a.err)->host = a.err_host;
+}
 
 // ------------------------------------------------------------------ work items
 // Tables of the groups in shared memory: rows [begin, end) and the tiles before.

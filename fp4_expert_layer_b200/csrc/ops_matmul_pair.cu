@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
     mbar_fence_init();
   }
   if (tid == 32 * 2) {
+    mm_set_mirror(a);
     tmap_prefetch(&a.wmap);
     tmap_prefetch(&a.xmap);
     mbar_init(smem_u32(&accf_bar[0]), 1);

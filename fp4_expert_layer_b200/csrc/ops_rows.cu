@@ -349,9 +349,9 @@ moe_status_t moe_combine_backward(const void *dy, int32_t dy_dtype, int64_t lddy
   moe_status_t st = check_shape(fn, T, k, H, rows);
   if (st != MOE_OK) return st;
   if (!is_float_dtype(dy_dtype) || !is_float_dtype(ys_dtype)) return ops_invalid(fn, "dtypes must be F32, BF16 or F16");
+  if (T == 0) return MOE_OK;
   if (!dys && !dgates) return ops_invalid(fn, "dys and dgates are both NULL");
   if (lddy < H || (dgates && ldys < H) || (dys && lddys < H)) return ops_invalid(fn, "row strides must be at least H");
-  if (T == 0) return MOE_OK;
   if (!dy || !inv || (dgates && !ys && rows > 0)) return ops_invalid(fn, "dy, inv and ys must be device pointers");
   if (!aligned_to(dy, dtype_bytes(dy_dtype)) || !aligned_to(ys, dtype_bytes(ys_dtype)) ||
       !aligned_to(dys, dtype_bytes(ys_dtype)))

@@ -28,13 +28,20 @@ from ._lib import MoEError, check, lib
 _DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, torch.uint8: 3}
 _BLOCK = {"mxfp4": 32, "nvfp4": 16}
 _U8, _I32, _F32 = torch.uint8, torch.int32, torch.float32
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 try:   # the allocation alone, without torch.empty's argument parsing (2.5 us of a small call's 10)
     from torch._C._dynamo.guards import _empty_strided_cuda as _empty_strided
 except ImportError:
     def _empty_strided(size, stride, dtype):
         return torch.empty_strided(size, stride, dtype=dtype, device="cuda")
+
+
+def _int32(fn, what, n):
+    """The C entry points take sizes as int32, which ctypes would cut silently."""
+    if n > 0x7FFFFFFF:
+        _bad(f"{fn}: {what} = {n} must be below 2^31")
 
 
 def _new(n, cols, dtype):
@@ -141,9 +148,10 @@ def fp4_quantize(x, fmt="mxfp4", rows_per_scale=None, out=None, stream=None):
         _bad(f"{fn}: format {fmt!r} is not 'mxfp4' or 'nvfp4'")
     shape, x2 = x.shape, x
     if len(shape) == 3:
-        if shape[0] > 1 and x.stride(0) != shape[1] * x.stride(1):
-            _bad(f"{fn}: the matrices of x must follow one another at the row stride")
-        x2 = x.flatten(0, 1)
+        try:
+            x2 = x.view(shape[0] * shape[1], shape[2])
+        except RuntimeError:
+            _bad(f"{fn}: the matrices of x must follow one another at one row stride")
         if rows_per_scale is None:
             rows_per_scale = max(1, shape[1])
     elif len(shape) != 2:
@@ -228,6 +236,8 @@ def fp4_matmul(x, w, offsets=None, out_dtype=torch.bfloat16, out=None, stream=No
     if len(lead) != 1 or len(wlead) not in (1, 2) or wK != K or wfmt != fmt:
         _bad(f"{fn}: x {list(xc.shape)} {x.fmt} and w {list(wc.shape)} {w.fmt} do not multiply")
     n, N = lead[0], wlead[-1]
+    if n > 0x7FFFFFFF or N > 0x7FFFFFFF or K > 0x7FFFFFFF:
+        _int32(fn, "a size", max(n, N, K))
     groups = wlead[0] if len(wlead) == 2 else 1
     if fmt:
         _want(fn, "x.global_scale", xg, _F32, (n,))
@@ -265,6 +275,8 @@ def sort_tokens(ids, n_experts, stream=None):
         _bad(f"sort_tokens: ids must be contiguous int32 [T, k], not {ids.dtype} {list(shape)}")
     T, k = shape
     E = int(n_experts)
+    if T * k > 0x7FFFFFFF:
+        _int32("sort_tokens", "T * k", T * k)
     if not 1 <= E <= 1024:
         _bad(f"sort_tokens: {E} experts: 1 to 1024 are supported")
     counts, offsets = _empty_strided((E,), (1,), _I32), _empty_strided((E + 1,), (1,), _I32)
@@ -281,6 +293,8 @@ def _pairs(fn, inv, T, dev, gates=None):
     shape = inv.shape
     if len(shape) != 2 or inv.dtype is not _I32 or not inv.is_contiguous() or (T is not None and shape[0] != T):
         _bad(f"{fn}: inv must be contiguous int32 [{'T' if T is None else T}, k], not {inv.dtype} {list(shape)}")
+    if shape[0] * shape[1] > 0x7FFFFFFF:
+        _int32(fn, "T * k", shape[0] * shape[1])
     if gates is not None:
         _want(fn, "gates", gates, _F32, shape)
     _same(fn, dev, inv, gates)
@@ -291,6 +305,8 @@ def _two(fn, name, t):
     shape = t.shape
     if len(shape) != 2:
         _bad(f"{fn}: {name} must have two axes, not {len(shape)}")
+    if shape[0] > 0x7FFFFFFF or shape[1] > 0x7FFFFFFF:
+        _int32(fn, f"an axis of {name}", max(shape))
     return shape
 
 
@@ -317,7 +333,9 @@ def dispatch(x, inv, rows=None, out=None, stream=None):
     if dt is None:
         _bad(f"{fn}: x must be float32, bfloat16, float16 or uint8, not {dtype}")
     if out is None:
-        rows = T * k if rows is None else rows
+        rows = T * k if rows is None else int(rows)
+        if not 0 <= rows <= 0x7FFFFFFF:
+            _bad(f"{fn}: rows = {rows} must be 0 to 2^31 - 1")
         out = _new(rows, H, dtype)
     else:
         rows = out.shape[0] if rows is None else rows

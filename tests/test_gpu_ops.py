@@ -315,6 +315,12 @@ def test_quantize_matrices_at_once():
         assert t.equal(q.codes[e], one.codes) and t.equal(q.scales[e], one.scales)
         assert q.global_scale[e] == one.global_scale[0]
     assert F.fp4_dequantize(q).shape == w.shape
+    first = F.fp4_quantize(w[:, :1], "nvfp4")              # one row of each matrix: a row stride of 40 rows
+    for e in range(3):
+        one = F.fp4_quantize(w[e, :1], "nvfp4")
+        assert t.equal(first.codes[e], one.codes) and first.global_scale[e] == one.global_scale[0]
+    with pytest.raises(F.MoEError):
+        F.fp4_quantize(w[:, :2], "nvfp4")
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
@@ -553,6 +559,46 @@ def test_graph_replays_the_path_and_streams_do_not_mix(fmt):
     t.cuda.synchronize()
     for y, r, a, gt in got:
         assert t.equal(y, F.combine(F.dispatch(a, r["inv"]), r["inv"], gt))
+
+
+def test_calls_with_no_rows():
+    t, F = G.torch(), G.library()
+    for fmt in ("mxfp4", "nvfp4"):
+        q = F.fp4_quantize(t.empty((0, 64), device="cuda"), fmt)
+        assert q.codes.shape == (0, 32) and F.fp4_dequantize(q).shape == (0, 64)
+        w = F.fp4_quantize(randn((8, 64), 1), fmt, rows_per_scale=8)
+        assert F.fp4_matmul(q, w).shape == (0, 8)
+        three = F.fp4_quantize(t.empty((3, 0, 64), device="cuda"), fmt)
+        assert three.codes.shape == (3, 0, 32)
+    none = t.empty((0, 4), dtype=t.int32, device="cuda")
+    x = t.empty((0, 24), device="cuda")
+    assert F.dispatch(x, none).shape == (0, 24) and F.combine(x, none).shape == (0, 24)
+    assert F.dispatch_backward(x, none).shape == (0, 24)
+    dys, dg = F.combine_backward(x, x, none)
+    assert dys.shape == (0, 24) and dg.shape == (0, 4)
+    # tokens, but no row: every pair is dropped
+    inv = t.full((5, 4), -1, dtype=t.int32, device="cuda")
+    assert F.dispatch(randn((5, 24), 2), inv, rows=0).shape == (0, 24)
+    assert (F.combine(x, inv) == 0).all() and (F.dispatch_backward(x, inv) == 0).all()
+    dys, dg = F.combine_backward(randn((5, 24), 3), x, inv)
+    assert dys.shape == (0, 24) and (dg == 0).all()
+
+
+def test_a_call_whose_tensors_are_not_on_the_current_device(monkeypatch):
+    """The detour that such a call takes, with a current device that is said to be another at first."""
+    t, F = G.torch(), G.library()
+    from fp4_expert_layer_b200 import ops
+    x = randn((6, 64), 4, "bf16")
+    want = F.fp4_quantize(x)
+    real, told = ops._current_device, []
+
+    def other_at_first():
+        told.append(1)
+        return 63 if len(told) == 1 else real()
+
+    monkeypatch.setattr(ops, "_current_device", other_at_first)
+    got = F.fp4_quantize(x)
+    assert len(told) == 2 and t.equal(got.codes, want.codes) and t.equal(got.scales, want.scales)
 
 
 def test_wide_products_on_two_streams_at_once():

@@ -105,7 +105,7 @@ def test_row_operators_refuse(F, fn, base, bad):
     ("moe_dispatch", DISPATCH, dict(rows=0, xs=None)),
     ("moe_dispatch_backward", DBWD, dict(T=0, dx=None)),
     ("moe_combine", COMBINE, dict(T=0, y=None)),
-    ("moe_combine_backward", CBWD, dict(T=0, dy=None, dg=None)),
+    ("moe_combine_backward", CBWD, dict(T=0, dy=None, dys=None, dg=None)),
 ])
 def test_nothing_to_do_is_a_no_op(F, fn, base, empty):
     assert getattr(F.lib(), fn)(*_args(base, **empty)) == 0
