@@ -9,9 +9,12 @@ loads the checked library when FP4MOE_CHECKED=1 is set in the environment.
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
+import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -19,6 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 SO = os.path.join(HERE, "libfp4moe.so")
 SO_CHECKED = os.path.join(HERE, "libfp4moe_checked.so")
+SO_BINDING = os.path.join(HERE, "_ops.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -43,7 +47,28 @@ def nvcc_cmd(out: str, extra=()):
              "--threads", "0", "-I", INCLUDE, "-I", CSRC, "-o", out] + list(extra) + sources())
 
 
+def build_binding(force: bool = False) -> str | None:
+    """The operators' torch binding; None where torch is not installed."""
+    if importlib.util.find_spec("torch") is None:
+        return None
+    src = os.path.join(CSRC, "ops_binding.cpp")
+    deps = [src] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not force and os.path.exists(SO_BINDING) and all(os.path.getmtime(d) <= os.path.getmtime(SO_BINDING) for d in deps):
+        return SO_BINDING
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which("nvcc"))))
+    tmp = SO_BINDING + f".tmp{os.getpid()}"
+    subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f'-DMOE_TORCH_VERSION="{torch.__version__}"',
+                    "-I", INCLUDE, "-I", os.path.join(root, "include"), "-I", os.path.join(cuda, "include"),
+                    "-I", sysconfig.get_paths()["include"], src, "-o", tmp, "-L", os.path.join(root, "lib"),
+                    "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"], check=True)
+    os.replace(tmp, SO_BINDING)
+    return SO_BINDING
+
+
 def build(force: bool = False, verbose: bool = False, checked: bool = False) -> str:
+    build_binding(force)
     so = SO_CHECKED if checked else SO
     if not force and up_to_date(so):
         return so
