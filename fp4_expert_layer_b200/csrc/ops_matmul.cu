@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
     tmem_relinquish();
   }
   wait_prior_grid();
-  mm_scan_groups<NT>(a, groups);
+  mm_scan_groups(a, groups);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -116,9 +116,12 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
     ranks = (int)cg::this_cluster().num_blocks();
     rank = (int)cg::this_cluster().block_rank();
   }
-  const int k0 = nk_all * rank / ranks, k1 = nk_all * (rank + 1) / ranks;
+  // ranges of whole steps of the scales, so that a step starts on a sector
+  constexpr int AHEAD = kSfAhead<WF>;
+  const int steps = (nk_all + AHEAD - 1) / AHEAD;
+  const int k0 = min(nk_all, steps * rank / ranks * AHEAD), k1 = min(nk_all, steps * (rank + 1) / ranks * AHEAD);
   const unsigned first = SPLIT ? blockIdx.x / (unsigned)ranks : blockIdx.x, step = SPLIT ? 0u : gridDim.x;
-  using Walk = MmWalk<NT>;
+  using Walk = MmWalk;
 
   if (warp == 0) {
     // ---------------- codes
@@ -234,6 +237,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
     const bool tokens = (warp & 1) != 0;
     constexpr int RG = (NT + 31) / 32 < 4 ? (NT + 31) / 32 : 4;        // 32-row groups of a token tile
     const uint8_t *rowp[4];
+    const uint8_t *lo = tokens ? a.xs : a.ws, *hi = lo + (tokens ? (size_t)a.rows : (size_t)a.groups * a.N) * a.nsf;
     const uint32_t off = Geo::SF_OFF + (tokens ? Geo::SF_BYTES : 0) + 16 * lane;
     feed_scales<WF, S, true>(
         a, groups, Walk(a, groups, nrb, first, step), k0, k1, (warp - 6) >> 1, 2,
@@ -243,7 +247,10 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
             rowp[j] = tokens ? a.xs + (size_t)min(m.row0 + 32 * j + lane, a.rows - 1) * a.nsf
                              : a.ws + ((size_t)m.g * a.N + min(m.rb * 128 + 32 * j + lane, a.N - 1)) * a.nsf;
         },
-        [&](int it0, uint32_t(&w)[4][8]) { fetch_sf<WF>(a, rowp, tokens ? RG : 4, it0, k1, w); },
+        [&](int it0, uint32_t(&w)[4][8]) {
+          if (a.sf_wide) fetch_sf<WF, true>(a, rowp, tokens ? RG : 4, it0, k1, lo, hi, w);
+          else fetch_sf<WF, false>(a, rowp, tokens ? RG : 4, it0, k1, lo, hi, w);
+        },
         [&](int s, uint32_t parity) { return mbar_wait_warp(smem_u32(&empty_bar[s]), parity, a.err, 65); },
         [&](const Walk &) {
           return [&](int s, const uint32_t(&w)[4][8], int i) {
@@ -429,12 +436,18 @@ extern "C" moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_
     return offsets ? std::min<int64_t>(rows, rows / nt + n_groups) : (rows + nt - 1) / nt;
   };
   const bool streamed = mean <= 32 && blocks >= sms, split = !streamed && mean <= 16;
-  const int nt = streamed ? 32 : split ? 16 : kPairRows;
+  // pairs: the smallest tile whose items still run at once, for its shorter
+  // epilogue; else the largest, which moves the least
+  const int64_t wide_blocks = (N + 255) / 256;
+  int nt = streamed ? 32 : split ? 16 : 64;
+  if (!streamed && !split)
+    while (nt < kPairRows && tiles(nt) * wide_blocks > sms / 2) nt *= 2;
+  if (nt >= 64 && tiles(nt) * wide_blocks > sms / 2) nt = kPairRows;
   const cuuint64_t kb = (cuuint64_t)(K / 2);
   const cuuint32_t ones[3] = {1, 1, 1};
   {
     const cuuint64_t dims[2] = {kb, (cuuint64_t)rows}, strides[1] = {kb};
-    const cuuint32_t box[2] = {128, (cuuint32_t)(nt == kPairRows ? kPairBox : nt)};
+    const cuuint32_t box[2] = {128, (cuuint32_t)(nt >= 64 ? kPairBox : nt)};
     if (enc(&a.xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(x_codes), dims, strides, box, ones,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -464,13 +477,10 @@ extern "C" moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_
   a.err = &err.dev->code;
   a.err_host = err.host;
   a.rows = rows; a.groups = n_groups; a.N = N; a.K = K;
+  while ((1 << a.tile_log) < nt) ++a.tile_log;
   a.nsf = K / (fmt == MOE_FMT_MXFP4 ? 32 : 16);
   a.dtype = dtype;
-  const int stage = fmt == MOE_FMT_MXFP4 ? 8 : 16;         // scale bytes of 256 K
-  a.sf_mode = a.nsf % stage == 0 && aligned_to(x_scales, stage) && aligned_to(w_scales, stage) ? 0
-              : a.nsf % 4 == 0 && aligned_to(x_scales, 4) && aligned_to(w_scales, 4)           ? 1
-                                                                                              : 2;
-  a.sf_wide = a.sf_mode == 0 && a.nsf % 16 == 0 && aligned_to(x_scales, 16) && aligned_to(w_scales, 16);
+  a.sf_wide = a.nsf % 16 == 0 && aligned_to(x_scales, 16) && aligned_to(w_scales, 16);
   a.y_vec = row_alignment(y, ldy * dtype_bytes(dtype)) >= 16;
   const bool mx = fmt == MOE_FMT_MXFP4;
   cudaError_t e;
@@ -479,14 +489,15 @@ extern "C" moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_
     e = mx ? launch_matmul<WF_MX, 32, false>(a, grid, 1, s) : launch_matmul<WF_NV, 32, false>(a, grid, 1, s);
   } else if (split) {
     // one item a cluster; as many ways as keep every cluster resident (a second
-    // round doubles the time) and leave each way two stages
+    // round doubles the time) and leave each way a step of the scales (four stages
+    // of MXFP4, two of NVFP4: four)
     const int64_t items = tiles(16) * ((N + 127) / 128);
     const int nk = (K + 255) / 256;
     int ranks = 1;
     while (ranks < 8 && items * ranks * 2 <= sms && nk >= 4 * ranks) ranks *= 2;
     e = mx ? launch_matmul<WF_MX, 16, true>(a, (int)items, ranks, s) : launch_matmul<WF_NV, 16, true>(a, (int)items, ranks, s);
   } else {
-    const int pairs = (int)std::min<int64_t>(tiles(kPairRows) * ((N + 255) / 256), sms / 2);
+    const int pairs = (int)std::min<int64_t>(tiles(nt) * wide_blocks, sms / 2);
     e = launch_matmul_pair(mx ? WF_MX : WF_NV, a, pairs, s);
   }
   return ops_launched(fn, e);

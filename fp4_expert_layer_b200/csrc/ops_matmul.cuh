@@ -23,9 +23,9 @@ struct MatmulArgs {
   int *err;                      // the device's error word (an ErrWord), which the waits poll
   int *err_host;                 // its mirror in mapped host memory
   int rows, groups, N, K;
+  int tile_log;                  // a token tile has 2^tile_log rows
   int nsf;                       // scales in a row
-  int sf_mode;                   // 0: a stage's scales in one load, 1: words of four, 2: bytes
-  int sf_wide;                   // 1: scale rows start on 16 bytes and are whole stages
+  int sf_wide;                   // 1: scale rows start on 16 bytes
   int dtype;
   int y_vec;                     // rows of y start on 16 bytes
 };
@@ -45,7 +45,6 @@ struct MmGroups {
 
 // Every CTA makes the tables for itself: thread t takes `per` consecutive groups.
 // Called by all threads; offsets are cut to [0, rows].
-template <int NT>
 __device__ __forceinline__ void mm_scan_groups(const MatmulArgs &a, MmGroups &t) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = blockDim.x;
   if (!a.offsets) {                                        // one group of all rows: no scan
@@ -53,7 +52,7 @@ __device__ __forceinline__ void mm_scan_groups(const MatmulArgs &a, MmGroups &t)
       t.begin[0] = 0;
       t.end[0] = a.rows;
       t.tiles[0] = 0;
-      t.tiles[1] = (a.rows + NT - 1) / NT;
+      t.tiles[1] = (a.rows + (1 << a.tile_log) - 1) >> a.tile_log;
     }
     return;
   }
@@ -66,7 +65,7 @@ __device__ __forceinline__ void mm_scan_groups(const MatmulArgs &a, MmGroups &t)
     t.begin[g] = b;
     t.end[g] = max(b, e);
     t.tiles[g] = sum;
-    sum += (max(b, e) - b + NT - 1) / NT;
+    sum += (max(b, e) - b + (1 << a.tile_log) - 1) >> a.tile_log;
   }
   int inc = sum;
 #pragma unroll
@@ -91,7 +90,6 @@ __device__ __forceinline__ void mm_scan_groups(const MatmulArgs &a, MmGroups &t)
 // A warp's walk over the items first, first + step, ...: item = tile * nrb + row
 // block, the tiles in group order.  Whole warps walk (the groups are searched 32
 // at a time); values are warp-uniform.
-template <int NT>
 struct MmWalk {
   int g, row0, nrows, rb;        // of the item: group, first row, rows, block of weight rows
   int tile, dtile, drb, nrb, ntiles;
@@ -123,68 +121,102 @@ struct MmWalk {
       g += __popc(passed);
       if (passed != 0xffffffffu) break;
     }
-    row0 = t.begin[g] + (tile - t.tiles[g]) * NT;
-    nrows = min(NT, t.end[g] - row0);
+    row0 = t.begin[g] + ((tile - t.tiles[g]) << a.tile_log);
+    nrows = min(1 << a.tile_log, t.end[g] - row0);
   }
 };
 
 // ---------------------------------------------------------------------- scales
-// The scales of one row for one stage (K elements 256 * it ..): WORDS words.
-// Columns past the row's end read as 1.0 (their codes are zero).
-template <int WORDS>
-__device__ __forceinline__ void load_sf(const uint8_t *row, int it, int nsf, int mode, uint32_t fill, uint32_t *w) {
-  const int c0 = it * WORDS * 4;
-  if (mode == 0) {
-    if constexpr (WORDS == 4) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row + c0));
-      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-    } else {
-      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row + c0));
-      w[0] = v.x; w[1] = v.y;
-    }
-  } else if (mode == 1) {
+// Rows of scales lie where nsf bytes a row put them: at any byte.  A lane reads 32
+// bytes of a row at a time, a whole sector of memory.
+
+// The aligned 16-byte pieces that hold the n bytes (up to 32) from p on.
+__device__ __forceinline__ void load_pieces(const uint8_t *p, int n, uint4 (&v)[3]) {
+  const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15u);
+  const uint4 *q = reinterpret_cast<const uint4 *>(p - off);
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i)
-      w[i] = c0 + 4 * i < nsf ? __ldg(reinterpret_cast<const uint32_t *>(row + c0 + 4 * i)) : fill;
-  } else {
+  for (int j = 0; j < 3; ++j) v[j] = 16 * j < off + n ? __ldg(q + j) : make_uint4(0u, 0u, 0u, 0u);
+}
+// Those bytes out of them, then `fill`, as eight words.
+__device__ __forceinline__ void shift_pieces(const uint8_t *p, int n, const uint4 (&v)[3], uint32_t fill,
+                                             uint32_t (&out)[8]) {
+  const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15u);
+  uint32_t w[12];
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i) {
-      w[i] = 0;
+  for (int j = 0; j < 3; ++j) { w[4 * j] = v[j].x; w[4 * j + 1] = v[j].y; w[4 * j + 2] = v[j].z; w[4 * j + 3] = v[j].w; }
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int c = c0 + 4 * i + b;
-        w[i] |= (c < nsf ? (uint32_t)__ldg(row + c) : (fill & 0xFFu)) << (8 * b);
-      }
-    }
+  for (int i = 0; i < 11; ++i) w[i] = off & 4 ? w[i + 1] : w[i];
+#pragma unroll
+  for (int i = 0; i < 9; ++i) w[i] = off & 8 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) out[i] = __funnelshift_r(w[i], w[i + 1], 8 * (off & 3));
+  if (n == 32) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int have = min(max(n - 4 * i, 0), 4);
+    const uint32_t mask = have == 4 ? 0xFFFFFFFFu : (1u << (8 * have)) - 1u;
+    out[i] = (out[i] & mask) | (fill & ~mask);
   }
 }
+
+// A scale of 1.0 four times: what the columns past a row's end have (their codes are zero).
 template <int WF>
 constexpr uint32_t kSfOne = WF == WF_MX ? 0x7F7F7F7Fu : 0x38383838u;
 
-// Scales come 32 bytes of a row at a time, a whole sector of memory: AHEAD stages.
 template <int WF>
 constexpr int kSfWords = WF == WF_MX ? 2 : 4;              // words of scales a row has in a stage
 template <int WF>
-constexpr int kSfAhead = 8 / kSfWords<WF>;
+constexpr int kSfAhead = 8 / kSfWords<WF>;                 // stages that 32 bytes of scales are
 
-// 32 bytes of four rows' scales from stage it0 on (as far as stage k1).
-template <int WF>
+// 32 bytes of `rows` (up to four) rows' scales from stage it0 on, as far as stage k1.
+// WIDE: scale rows start on 16 bytes.
+template <int WF, bool WIDE>
 __device__ __forceinline__ void fetch_sf(const MatmulArgs &a, const uint8_t *const (&row)[4], int rows, int it0, int k1,
-                                         uint32_t (&w)[4][8]) {
-  constexpr int WORDS = kSfWords<WF>, AHEAD = kSfAhead<WF>;
+                                         const uint8_t *lo, const uint8_t *hi, uint32_t (&w)[4][8]) {
+  const int c0 = it0 * 4 * kSfWords<WF>, n = min(32, min(k1 * 4 * kSfWords<WF>, a.nsf) - c0);
+  if constexpr (WIDE) {                                    // n is a multiple of 8; rows go on in 16s
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j >= rows) break;
+      const uint4 *p = reinterpret_cast<const uint4 *>(row[j] + c0);
+      const uint4 one = make_uint4(kSfOne<WF>, kSfOne<WF>, kSfOne<WF>, kSfOne<WF>);
+      const uint4 x = __ldg(p), y = n > 16 ? __ldg(p + 1) : one;
+      w[j][0] = x.x; w[j][1] = x.y; w[j][2] = x.z; w[j][3] = x.w;
+      w[j][4] = y.x; w[j][5] = y.y; w[j][6] = y.z; w[j][7] = y.w;
+    }
+    return;
+  }
+  // do the pieces reach past the scales' ends?
+  bool past = false;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (j >= rows) break;
-    if (a.sf_wide && it0 + AHEAD <= k1) {
-      const uint4 *p = reinterpret_cast<const uint4 *>(row[j] + it0 * 4 * WORDS);
-      const uint4 lo = __ldg(p), hi = __ldg(p + 1);
-      w[j][0] = lo.x; w[j][1] = lo.y; w[j][2] = lo.z; w[j][3] = lo.w;
-      w[j][4] = hi.x; w[j][5] = hi.y; w[j][6] = hi.z; w[j][7] = hi.w;
-      continue;
-    }
+    const uint8_t *p = row[j] + c0;
+    const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15u);
+    past = past || p - off < lo || p - off + (off + n + 15) / 16 * 16 > hi;
+  }
+  if (!__any_sync(0xffffffffu, past)) {
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i)
-      if (it0 + i < k1) load_sf<WORDS>(row[j], it0 + i, a.nsf, a.sf_mode, kSfOne<WF>, &w[j][i * WORDS]);
+    for (int j = 0; j < 4; j += 2) {                       // two rows' loads in flight together
+      if (j >= rows) break;
+      uint4 v0[3], v1[3];
+      load_pieces(row[j] + c0, n, v0);
+      if (j + 1 < rows) load_pieces(row[j + 1] + c0, n, v1);
+      shift_pieces(row[j] + c0, n, v0, kSfOne<WF>, w[j]);
+      if (j + 1 < rows) shift_pieces(row[j + 1] + c0, n, v1, kSfOne<WF>, w[j + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {                          // byte by byte: the first and last rows alone
+      if (j >= rows) break;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        w[j][i] = 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          w[j][i] |= (4 * i + b < n ? (uint32_t)__ldg(row[j] + c0 + 4 * i + b) : kSfOne<WF> & 0xFFu) << (8 * b);
+      }
+    }
   }
 }
 
@@ -250,9 +282,9 @@ __device__ __forceinline__ void store_out(void *y, int dtype, int64_t at, float 
   else static_cast<uint16_t *>(y)[at] = f16_bits(v);
 }
 
-// The pair kernel (ops_matmul_pair.cu): items of 256 rows x 256 weight rows.
+// The pair kernel (ops_matmul_pair.cu): items of 64, 128 or 256 rows x 256 weight rows.
 cudaError_t launch_matmul_pair(int wf, const MatmulArgs &a, int pairs, cudaStream_t s);
-constexpr int kPairRows = 256;        // rows of a token tile
+constexpr int kPairRows = 256;        // rows of a token tile at most
 constexpr int kPairBox = 64;          // rows of its TMA boxes
 
 }  // namespace moe

@@ -57,7 +57,7 @@ struct PairGeom {
   static_assert(SMEM + 13 * 1024 <= 227 * 1024, "shared-memory budget");
 };
 
-template <int WF>
+template <int WF, bool WIDE>
 __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const __grid_constant__ MatmulArgs a) {
   using Geo = PairGeom<WF>;
   constexpr int S = Geo::STAGES, WORDS = kSfWords<WF>, NBLK = Geo::NBLK;
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
     tmem_relinquish_pair();
   }
   wait_prior_grid();
-  mm_scan_groups<kPairRows>(a, groups);
+  mm_scan_groups(a, groups);
   tc_fence_before();
   __syncthreads();
   cluster.sync();                                          // both CTAs' barriers and TMEM are ready
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
   const int nrb = (a.N + 255) / 256;
   const int nk = (a.K + 255) / 256;
   const unsigned first = blockIdx.x >> 1, step = gridDim.x >> 1;
-  using Walk = MmWalk<kPairRows>;
+  using Walk = MmWalk;
 
   if (warp == 0) {
     // ---------------- codes of this CTA's rows; their bytes count on the even CTA's barrier
@@ -289,6 +289,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
     const uint32_t off = (which == 0 ? Geo::SFA_OFF : Geo::SFB_OFF + 512 * (which - 1)) + 16 * lane;
     const int pitch = which == 0 ? 512 : 1024;             // between a stage's blocks
     const uint8_t *rowp[4];
+    const uint8_t *lo = which ? a.xs : a.ws, *hi = lo + (which ? (size_t)a.rows : (size_t)a.groups * a.N) * a.nsf;
     bool wanted = false;                                   // the second half of a narrow tile is not read
     feed_scales<WF, S, false>(
         a, groups, Walk(a, groups, nrb, first, step), 0, nk, 0, 1,
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
                           ? a.ws + ((size_t)m.g * a.N + min(m.rb * 256 + (int)rank * 128 + 32 * j + lane, a.N - 1)) * a.nsf
                           : a.xs + (size_t)min(m.row0 + 128 * (which - 1) + 32 * j + lane, a.rows - 1) * a.nsf;
         },
-        [&](int it0, uint32_t(&w)[4][8]) { fetch_sf<WF>(a, rowp, wanted ? 4 : 0, it0, nk, w); },
+        [&](int it0, uint32_t(&w)[4][8]) { fetch_sf<WF, WIDE>(a, rowp, wanted ? 4 : 0, it0, nk, lo, hi, w); },
         [&](int s, uint32_t parity) { return mbar_wait_warp(smem_u32(&empty_bar[s]), parity, a.err, 75); },
         [&](const Walk &) {
           return [&, store = wanted](int s, const uint32_t(&w)[4][8], int i) {
@@ -326,10 +327,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
   }
 }
 
-template <int WF>
+template <int WF, bool WIDE>
 cudaError_t launch_pair(const MatmulArgs &a, int pairs, cudaStream_t s) {
   using Geo = PairGeom<WF>;
-  auto fn = fp4_matmul_pair_kernel<WF>;
+  auto fn = fp4_matmul_pair_kernel<WF, WIDE>;
   static std::atomic<uint64_t> asked{0};
   const cudaError_t e = ask_shared(fn, Geo::SMEM, asked);
   if (e != cudaSuccess) return e;
@@ -353,7 +354,10 @@ cudaError_t launch_pair(const MatmulArgs &a, int pairs, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_matmul_pair(int wf, const MatmulArgs &a, int pairs, cudaStream_t s) {
-  return wf == WF_MX ? launch_pair<WF_MX>(a, pairs, s) : launch_pair<WF_NV>(a, pairs, s);
+  // scale rows at any byte take registers that cost the others a tenth (grouped
+  // prefill 71 us; 66 with the kernel that has them on 16 bytes)
+  if (wf == WF_MX) return a.sf_wide ? launch_pair<WF_MX, true>(a, pairs, s) : launch_pair<WF_MX, false>(a, pairs, s);
+  return a.sf_wide ? launch_pair<WF_NV, true>(a, pairs, s) : launch_pair<WF_NV, false>(a, pairs, s);
 }
 
 }  // namespace moe

@@ -377,7 +377,8 @@ def _check_product(x, w, offsets, y0, y, out):
 
 
 DENSE = [(1, 1, 32), (1, 4096, 4096), (2, 127, 96), (7, 128, 256), (16, 130, 288), (17, 256, 512), (33, 64, 2048),
-         (65, 384, 1056), (128, 129, 160), (129, 256, 320), (300, 200, 1024), (1000, 512, 768), (3, 2048, 8224)]
+         (65, 384, 1056), (128, 129, 160), (129, 256, 320), (300, 200, 1024), (1000, 512, 768), (3, 2048, 8224),
+         (1, 300, 2560), (2, 256, 3584), (16, 512, 1536), (5, 128, 5632), (9, 130, 6720), (4, 64, 2304)]
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
