@@ -12,7 +12,7 @@
 //
 // Measured, bf16, 8192 tokens x 8 pairs, H 2048 (share of the copy rate): dispatch
 // 48.7 us (94%), its backward 51.2 (90%), combine 52.0 (89%), its backward 97.8
-// (89%); 33 tokens 2.2 to 4.2 us.  More rows in flight a warp (8, or wider columns)
+// (89%); 33 tokens 2.2 to 3.0 us.  More rows in flight a warp (8, or wider columns)
 // cost registers and with them warps: 59 to 74 us for combine.
 #include "ops_common.cuh"
 
@@ -187,11 +187,11 @@ struct CombineBwdArgs {
   const int *inv;
   const float *gates;     // NULL: ones
   int64_t lddy, ldys, lddys;
-  int T, k, rows, H, chunks;
+  int T, k, rows, H, chunks, pairs;
 };
 
-// A CTA takes one token; its warps take the 256-column chunks in turn.  A warp
-// keeps its chunk of dy in registers over the token's pairs: the pair's row of ys
+// A CTA takes one token and `pairs` of its pairs; its warps take the 256-column
+// chunks in turn.  A warp keeps its chunk of dy in registers over the token's pairs: the pair's row of ys
 // gives a partial of its gate's gradient, gate * dy goes out as its row of dys.
 template <typename TD, typename TS, bool VEC>
 __global__ void __launch_bounds__(256) combine_bwd_kernel(const CombineBwdArgs a) {
@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const CombineBwdArgs a
   const auto *dy = static_cast<const typename TD::raw *>(a.dy);
   const auto *ys = static_cast<const typename TS::raw *>(a.ys);
   auto *dys = static_cast<typename TS::raw *>(a.dys);
+  const int jb = blockIdx.y * a.pairs, je = min(a.k, jb + a.pairs);
   for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
     const int pos = lane < a.k ? __ldg(a.inv + t * a.k + lane) : -1;
     const float gate = lane < a.k && a.gates ? __ldg(a.gates + t * a.k + lane) : 1.0f;
@@ -209,13 +210,13 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const CombineBwdArgs a
       const int c0 = c * kCols;
       Lane8<TD, VEC> d;
       d.load(dy + t * a.lddy, c0, a.H, lane);
-      for (int j0 = 0; j0 < a.k; j0 += 4) {
+      for (int j0 = jb; j0 < je; j0 += 4) {
         Lane8<TS, VEC> v[4];
         int r[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           r[u] = __shfl_sync(0xffffffffu, pos, (j0 + u) & 31);
-          if (j0 + u >= a.k || r[u] >= a.rows) r[u] = -1;
+          if (j0 + u >= je || r[u] >= a.rows) r[u] = -1;
           if (r[u] >= 0 && a.dgates) v[u].load(ys + (int64_t)r[u] * a.ldys, c0, a.H, lane);
         }
 #pragma unroll
@@ -242,10 +243,11 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const CombineBwdArgs a
     if (!a.dgates) continue;
     part[warp][lane] = mine;
     __syncthreads();
-    if (threadIdx.x < a.k) {
+    const int j = jb + threadIdx.x;
+    if (j < je) {
       float s = 0.0f;
-      for (int w = 0; w < W; ++w) s += part[w][threadIdx.x];
-      a.dgates[t * a.k + threadIdx.x] = s;
+      for (int w = 0; w < W; ++w) s += part[w][j];
+      a.dgates[t * a.k + j] = s;
     }
     __syncthreads();
   }
@@ -258,8 +260,11 @@ cudaError_t launch_combine_bwd(CombineBwdArgs a, bool vec, cudaStream_t s) {
   // fewer waits at the barrier (8192 tokens x 8, H 2048, bf16: 104 us with 8, 98
   // with 4, 99 with 2; 33 tokens: 4.2, 6.5, 11.5)
   const int W = std::min(a.T >= 8 * sm_count() ? 4 : 8, a.chunks);
-  return launch_op(vec ? combine_bwd_kernel<TD, TS, true> : combine_bwd_kernel<TD, TS, false>,
-                   dim3((unsigned)std::min(a.T, 1 << 20)), 32 * W, 0, s, a);
+  // fewer tokens than SMs: four pairs to a CTA (33 tokens x 8, H 2048, bf16: 3.0 us,
+  // with all pairs to a CTA 4.2)
+  a.pairs = a.T < sm_count() ? 4 : a.k;
+  const dim3 grid((unsigned)std::min(a.T, 1 << 20), (unsigned)((a.k + a.pairs - 1) / a.pairs));
+  return launch_op(vec ? combine_bwd_kernel<TD, TS, true> : combine_bwd_kernel<TD, TS, false>, grid, 32 * W, 0, s, a);
 }
 
 // ------------------------------------------------------------ argument checks
@@ -356,7 +361,7 @@ moe_status_t moe_combine_backward(const void *dy, int32_t dy_dtype, int64_t lddy
   if (!aligned_to(dy, dtype_bytes(dy_dtype)) || !aligned_to(ys, dtype_bytes(ys_dtype)) ||
       !aligned_to(dys, dtype_bytes(ys_dtype)))
     return ops_invalid(fn, "dy, ys and dys must be aligned to their type");
-  CombineBwdArgs a{dy, ys, dys, dgates, inv, gates, lddy, ldys, lddys, T, k, rows, H, 0};
+  CombineBwdArgs a{dy, ys, dys, dgates, inv, gates, lddy, ldys, lddys, T, k, rows, H, 0, 0};
   const bool vec = vec_rows(dy, lddy, dy_dtype) && (!dgates || vec_rows(ys, ldys, ys_dtype)) &&
                    vec_rows(dys, lddys, ys_dtype);
   cudaStream_t s = static_cast<cudaStream_t>(stream);

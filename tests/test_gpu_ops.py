@@ -256,7 +256,7 @@ def _hard_rows(n, K, seed):
 @pytest.mark.parametrize("n, K, per, pad, shift", [
     (1, 32, 1, 0, 0), (3, 64, 1, 0, 0), (8, 2048, 1, 0, 0), (257, 96, 1, 0, 0), (5, 4128, 1, 8, 8), (4, 544, 1, 3, 1),
     (2, 32800, 1, 0, 0), (64, 256, 16, 0, 0), (6, 160, 2, 0, 0), (1024, 2048, 1024, 0, 0), (12, 96, 4, 2, 2),
-    (700, 1024, 350, 0, 0),
+    (700, 1024, 350, 0, 0), (64, 256, 16, 16, 0), (8, 128, 8, 0, 1), (600, 1312, 2, 0, 0), (1200, 1024, 8, 0, 0),
 ])
 def test_quantize_is_exact(dtype, fmt, n, K, per, pad, shift):
     t, F = G.torch(), G.library()
@@ -277,8 +277,8 @@ def test_quantize_is_exact(dtype, fmt, n, K, per, pad, shift):
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
-@pytest.mark.parametrize("per", [1, 4])
-def test_quantize_at_the_ends_of_the_range(fmt, per):
+@pytest.mark.parametrize("per, pad", [(1, 0), (4, 0), (4, 16), (8, 1)])
+def test_quantize_at_the_ends_of_the_range(fmt, per, pad):
     """The largest and smallest floats, infinities, NaN; blocks that are not finite become NaN alone."""
     t, F = G.torch(), G.library()
     x = np.zeros((8, 128), dtype=np.float32)
@@ -293,7 +293,7 @@ def test_quantize_at_the_ends_of_the_range(fmt, per):
     x[6, :64] = 1e-30
     x[6, 64:] = 1e30
     x[7] = -0.0
-    q = F.fp4_quantize(t.from_numpy(x).cuda(), fmt, rows_per_scale=per)
+    q = F.fp4_quantize(placed(t.from_numpy(x).cuda(), pad, 0), fmt, rows_per_scale=per)
     codes, scales, Gs, vals = ref.quantize(x.astype(np.float64), fmt, per)
     assert np.array_equal(q.scales.cpu().numpy(), scales.reshape(8, -1))
     if fmt == "nvfp4":
