@@ -5,9 +5,9 @@
 // Two CTAs of a cluster share one MMA of 256 weight rows x up to 256 token rows
 // (cta_group::2): each holds 128 weight rows and half the tokens' rows, so that a
 // stage of 256 K elements brings 32 KB of codes to an SM for 128 x 256 x 256
-// multiply-adds.  One CTA's 128 x 128 tile brings the same for half of them, and
-// what bounds the product is this fill, L2 to shared memory (about 45 bytes a
-// clock an SM reach it), not the tensor pipe.
+// multiply-adds.  One CTA's 128 x 128 tile brings the same for half of them, and is
+// then bound by this fill, L2 to shared memory (some 50 bytes a clock an SM), at half
+// of what the tensor pipe does.
 //
 // Measured: 8192 x 4096 x 4096, MXFP4, fp32 result 63.4 us (4.3 PFLOP/s; the MMAs
 // alone, with no operand copied, 51.7; under a second of load the power cap takes
