@@ -43,14 +43,13 @@ inline int row_alignment(const void *p, int64_t ld_bytes) {
 
 // The current device's SM count, looked up once per device.
 inline int sm_count() {
-  static int n[64] = {};
-  int dev = 0;
+  static std::atomic<int> known[64];
+  int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-  if (!n[dev]) {
-    int v = 0;
-    n[dev] = cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && v > 0 ? v : 148;
-  }
-  return n[dev];
+  if ((n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) n = 148;
+  known[dev].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 // Shared memory above 48 KB has to be asked for, once per kernel and device

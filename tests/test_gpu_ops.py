@@ -256,7 +256,7 @@ def _hard_rows(n, K, seed):
 @pytest.mark.parametrize("n, K, per, pad, shift", [
     (1, 32, 1, 0, 0), (3, 64, 1, 0, 0), (8, 2048, 1, 0, 0), (257, 96, 1, 0, 0), (5, 4128, 1, 8, 8), (4, 544, 1, 3, 1),
     (2, 32800, 1, 0, 0), (64, 256, 16, 0, 0), (6, 160, 2, 0, 0), (1024, 2048, 1024, 0, 0), (12, 96, 4, 2, 2),
-    (700, 1024, 350, 0, 0), (64, 256, 16, 16, 0), (8, 128, 8, 0, 1), (600, 1312, 2, 0, 0), (1200, 1024, 8, 0, 0),
+    (700, 1024, 350, 0, 0), (64, 256, 16, 16, 0), (8, 128, 8, 0, 1), (600, 1312, 2, 0, 0), (1200, 1024, 8, 0, 0), (48, 4096, 16, 0, 0),
 ])
 def test_quantize_is_exact(dtype, fmt, n, K, per, pad, shift):
     t, F = G.torch(), G.library()
@@ -681,6 +681,29 @@ def test_more_than_2_31_elements():
     y = F.fp4_matmul(x, w)
     last = F.FP4Tensor(x.codes[-tail:].clone(), x.scales[-tail:].clone(), None, "mxfp4")
     assert t.equal(y[-tail:], F.fp4_matmul(last, w))
+
+
+def test_quantize_and_long_sort_in_a_graph():
+    """The forms of several launches: each replay starts its counts and scales anew."""
+    t, F = G.torch(), G.library()
+    E, k = 300, 8
+    x = t.empty((3, 600, 1024), dtype=t.bfloat16, device="cuda")
+    ids = t.empty((4000, k), dtype=t.int32, device="cuda")
+    inputs = [(randn(x.shape, 64 + i, "bf16", s), ids_of(4000, k, E, 66 + i, -1, E + 1)) for i, s in
+              enumerate((50.0, 0.01))]
+    x.copy_(inputs[0][0])
+    ids.copy_(inputs[0][1])
+    g = t.cuda.CUDAGraph()
+    with t.cuda.graph(g):
+        q, r = F.fp4_quantize(x, "nvfp4"), F.sort_tokens(ids, E)
+    for a, i in inputs + inputs[:1]:
+        x.copy_(a)
+        ids.copy_(i)
+        g.replay()
+        t.cuda.synchronize()
+        want, order = F.fp4_quantize(a, "nvfp4"), F.sort_tokens(i, E)
+        assert all(t.equal(m, n) for m, n in zip(q[:3], want[:3]))
+        assert all(t.equal(r[n], order[n]) for n in order)
 
 
 def test_backward_in_a_graph():
