@@ -11,7 +11,7 @@
 // registers in ascending j: no atomics, one rounding, the same bits each time.
 //
 // Measured, bf16, 8192 tokens x 8 pairs, H 2048 (share of the copy rate): dispatch
-// 48.7 us (94%), its backward 51.2 (90%), combine 52.0 (89%), its backward 97.8
+// 48.7 us (94%), its backward 48.7 (95%), combine 48.9 (94%), its backward 97.8
 // (89%); 33 tokens 2.2 to 3.0 us.  More rows in flight a warp (8, or wider columns)
 // cost registers and with them warps: 59 to 74 us for combine.
 #include "ops_common.cuh"
@@ -24,7 +24,9 @@ namespace {
 // l, l + 32, ..., so that narrow accesses still coalesce.
 constexpr int kCols = 256;
 
-template <typename T, bool VEC>
+// STREAM: the rows are read once and the results written once, and take no place in
+// the caches that others would use.
+template <typename T, bool VEC, bool STREAM = false>
 struct Lane8 {
   alignas(16) typename T::raw v[8];
   __device__ __forceinline__ void load(const typename T::raw *row, int c0, int H, int lane) {
@@ -34,7 +36,7 @@ struct Lane8 {
         uint4 *w = reinterpret_cast<uint4 *>(v);
         const uint4 *p = reinterpret_cast<const uint4 *>(row + c);
 #pragma unroll
-        for (int i = 0; i < (int)(sizeof(v) / 16); ++i) w[i] = __ldg(p + i);
+        for (int i = 0; i < (int)(sizeof(v) / 16); ++i) w[i] = STREAM ? __ldcs(p + i) : __ldg(p + i);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = c + i < H ? __ldg(row + c + i) : typename T::raw(0);
@@ -54,7 +56,10 @@ struct Lane8 {
         const uint4 *w = reinterpret_cast<const uint4 *>(v);
         uint4 *p = reinterpret_cast<uint4 *>(row + c);
 #pragma unroll
-        for (int i = 0; i < (int)(sizeof(v) / 16); ++i) p[i] = w[i];
+        for (int i = 0; i < (int)(sizeof(v) / 16); ++i) {
+          if constexpr (STREAM) __stcs(p + i, w[i]);
+          else p[i] = w[i];
+        }
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -130,7 +135,8 @@ struct CombineOpArgs {
 };
 
 // A warp sums 256 columns of one token over its pairs.  The rows of four pairs
-// are loaded before the first is used.
+// are loaded before the first is used.  (As streams 48.9 us of 8192 x 8, H 2048, bf16,
+// else 51.8; the backward pass loses by it, 105 and 98.)
 template <typename TI, typename TO, bool VEC>
 __global__ void __launch_bounds__(128) combine_op_kernel(const CombineOpArgs a) {
   const int lane = threadIdx.x & 31;
@@ -147,7 +153,7 @@ __global__ void __launch_bounds__(128) combine_op_kernel(const CombineOpArgs a) 
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
     for (int j0 = 0; j0 < a.k; j0 += 4) {
-      Lane8<TI, VEC> v[4];
+      Lane8<TI, VEC, true> v[4];
       int r[4];
       float g[4];
 #pragma unroll
@@ -164,7 +170,7 @@ __global__ void __launch_bounds__(128) combine_op_kernel(const CombineOpArgs a) 
         for (int i = 0; i < 8; ++i) acc[i] = fmaf(g[u], v[u].get(i), acc[i]);
       }
     }
-    Lane8<TO, VEC> out;
+    Lane8<TO, VEC, true> out;
 #pragma unroll
     for (int i = 0; i < 8; ++i) out.set(i, acc[i]);
     out.store(y + t * a.ldy, c0, a.H, lane);
