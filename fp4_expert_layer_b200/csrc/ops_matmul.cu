@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
   __shared__ __align__(8) uint64_t acce_bar[NBUF];
   __shared__ __align__(8) uint64_t quiesce_bar;
   __shared__ uint32_t tmem_base_s;
+  __shared__ float xG_s[SPLIT ? NT : 1];
   __shared__ MmGroups groups;
 
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(mm_raw) + 1023) & ~uintptr_t(1023));
@@ -100,6 +101,15 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
     tmem_alloc(smem_u32(&tmem_base_s), 512);
     tmem_relinquish();
   }
+  const int nrb = (a.N + 127) / 128, nk_all = (a.K + 255) / 256;
+
+  // SPLIT: cluster c takes item c and rank r of it the K range [k0, k1)
+  const int rlog = SPLIT ? a.rank_log : 0, ranks = 1 << rlog, rank = SPLIT ? (int)cg::this_cluster().block_rank() : 0;
+  // ranges of whole steps of the scales, so that a step starts on a sector
+  constexpr int AHEAD = kSfAhead<WF>;
+  const int steps = (nk_all + AHEAD - 1) / AHEAD;
+  const int k0 = min(nk_all, (steps * rank >> rlog) * AHEAD), k1 = min(nk_all, (steps * (rank + 1) >> rlog) * AHEAD);
+  const unsigned first = blockIdx.x >> rlog, step = SPLIT ? 0u : gridDim.x;
   wait_prior_grid();
   mm_scan_groups(a, groups);
   tc_fence_before();
@@ -107,20 +117,6 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
   tc_fence_after();
   const uint32_t tmem = tmem_base_s;
   if constexpr (SPLIT) cluster_arrive();                   // this CTA's shared memory may be written from now on
-  const int nrb = (a.N + 127) / 128;
-  const int nk_all = (a.K + 255) / 256;
-
-  // SPLIT: cluster c takes item c and rank r of it the K range [k0, k1)
-  int ranks = 1, rank = 0;
-  if constexpr (SPLIT) {
-    ranks = (int)cg::this_cluster().num_blocks();
-    rank = (int)cg::this_cluster().block_rank();
-  }
-  // ranges of whole steps of the scales, so that a step starts on a sector
-  constexpr int AHEAD = kSfAhead<WF>;
-  const int steps = (nk_all + AHEAD - 1) / AHEAD;
-  const int k0 = min(nk_all, steps * rank / ranks * AHEAD), k1 = min(nk_all, steps * (rank + 1) / ranks * AHEAD);
-  const unsigned first = SPLIT ? blockIdx.x / (unsigned)ranks : blockIdx.x, step = SPLIT ? 0u : gridDim.x;
   using Walk = MmWalk;
 
   if (warp == 0) {
@@ -273,14 +269,16 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
     const Walk m(a, groups, nrb, first, step);
     const bool any = m.more();                             // the same for the whole cluster
     bool ok = k1 > k0;                                     // a rank without stages adds nothing
+    const float wG = (WF == WF_NV && any) ? __ldg(a.wG + m.g) : 1.0f;       // on their way while the products end
+    if (WF == WF_NV && any && tid < m.nrows) xG_s[tid] = __ldg(a.xG + m.row0 + tid);
     if (any && warp >= 2 && warp < 6) ok = mbar_wait_warp(smem_u32(&accf_bar[0]), 0, a.err, 66) && ok;
     __syncwarp();
     cluster_wait();                                        // every rank has begun (long ago)
-    const int per = 128 / ranks;                           // ranks is a power of two
+    const int plog = 7 - rlog, per = 1 << plog;
     if (any && warp >= 2 && warp < 6) {
       tc_fence_after();
       const int quad = warp & 3, row = 32 * quad + lane;
-      float *dst = cluster.map_shared_rank(recv, row / per) + ((size_t)rank * per + row % per) * NT;
+      float *dst = cluster.map_shared_rank(recv, row >> plog) + ((size_t)rank * per + (row & (per - 1))) * NT;
 #pragma unroll 1
       for (int c0 = 0; c0 < NT; c0 += 16) {
         uint32_t v[16];
@@ -296,13 +294,12 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
     }
     cluster.sync();                                        // every part is where it is added
     if (any) {
-      const float wG = (WF == WF_NV) ? __ldg(a.wG + m.g) : 1.0f;
       for (int i = tid; i < per * m.nrows; i += kMmThreads) {
-        const int c = i / per, r = i - c * per;            // neighbouring threads: neighbouring columns of y
+        const int c = i >> plog, r = i & (per - 1);            // neighbouring threads: neighbouring columns of y
         float v = 0.0f;
         for (int q = 0; q < ranks; ++q) v += recv[((size_t)q * per + r) * NT + c];
         const int col = m.rb * 128 + rank * per + r;
-        const float sc = (WF == WF_NV) ? wG * __ldg(a.xG + m.row0 + c) : 1.0f;
+        const float sc = (WF == WF_NV) ? wG * xG_s[c] : 1.0f;
         if (col < a.N) store_out(a.y, a.dtype, (int64_t)(m.row0 + c) * a.ldy + col, v * sc);
       }
     }
@@ -368,14 +365,14 @@ moe_status_t matmul_error_word(const char *fn, MatmulErr *out) {
 }
 
 template <int WF, int NT, bool SPLIT>
-cudaError_t launch_matmul(const MatmulArgs &a, int grid, int ranks, cudaStream_t s) {
+cudaError_t launch_matmul(const MatmulArgs &a, int items, cudaStream_t s) {
   using Geo = MmGeom<WF, NT, SPLIT>;
   auto fn = fp4_matmul_kernel<WF, NT, SPLIT>;
   static std::atomic<uint64_t> asked{0};
   const cudaError_t e = ask_shared(fn, Geo::SMEM, asked);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(grid * ranks));
+  cfg.gridDim = dim3((unsigned)items << a.rank_log);
   cfg.blockDim = dim3(kMmThreads);
   cfg.dynamicSmemBytes = Geo::SMEM;
   cfg.stream = s;
@@ -383,7 +380,7 @@ cudaError_t launch_matmul(const MatmulArgs &a, int grid, int ranks, cudaStream_t
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)ranks;
+  attr[1].val.clusterDim.x = 1u << a.rank_log;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
@@ -486,16 +483,15 @@ extern "C" moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_
   cudaError_t e;
   if (streamed) {
     const int grid = (int)std::min<int64_t>(tiles(32) * ((N + 127) / 128), sms);
-    e = mx ? launch_matmul<WF_MX, 32, false>(a, grid, 1, s) : launch_matmul<WF_NV, 32, false>(a, grid, 1, s);
+    e = mx ? launch_matmul<WF_MX, 32, false>(a, grid, s) : launch_matmul<WF_NV, 32, false>(a, grid, s);
   } else if (split) {
     // one item a cluster; as many ways as keep every cluster resident (a second
     // round doubles the time) and leave each way a step of the scales (four stages
     // of MXFP4, two of NVFP4: four)
     const int64_t items = tiles(16) * ((N + 127) / 128);
     const int nk = (K + 255) / 256;
-    int ranks = 1;
-    while (ranks < 8 && items * ranks * 2 <= sms && nk >= 4 * ranks) ranks *= 2;
-    e = mx ? launch_matmul<WF_MX, 16, true>(a, (int)items, ranks, s) : launch_matmul<WF_NV, 16, true>(a, (int)items, ranks, s);
+    while (a.rank_log < 3 && items << (a.rank_log + 1) <= sms && nk >= 4 << a.rank_log) ++a.rank_log;
+    e = mx ? launch_matmul<WF_MX, 16, true>(a, (int)items, s) : launch_matmul<WF_NV, 16, true>(a, (int)items, s);
   } else {
     const int pairs = (int)std::min<int64_t>(tiles(nt) * wide_blocks, sms / 2);
     e = launch_matmul_pair(mx ? WF_MX : WF_NV, a, pairs, s);

@@ -28,6 +28,7 @@ struct MatmulArgs {
   int sf_wide;                   // 1: scale rows start on 16 bytes
   int dtype;
   int y_vec;                     // rows of y start on 16 bytes
+  int rank_log;                  // 2^rank_log CTAs of a cluster share an item's K
 };
 
 // The error word knows its mirror; every CTA says so before it waits for anything.
