@@ -111,6 +111,11 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
   const int k0 = min(nk_all, (steps * rank >> rlog) * AHEAD), k1 = min(nk_all, (steps * (rank + 1) >> rlog) * AHEAD);
   const unsigned first = blockIdx.x >> rlog, step = SPLIT ? 0u : gridDim.x;
   wait_prior_grid();
+  // Few rows: the next kernel is small too and may be placed now (products one after
+  // another 6.0 -> 5.75 us).  Not after the streamed kernel: a wide kernel placed
+  // early crowds the SMs that are free first (32 x 8 tokens, two products and what
+  // lies between them: 73 -> 75 us).
+  if (SPLIT) trigger_dependents();
   mm_scan_groups(a, groups);
   tc_fence_before();
   __syncthreads();
