@@ -20,7 +20,7 @@
 // rank order through distributed shared memory.
 //
 // Measured: 256 rows over 64 groups, N = K = 2048, NVFP4: 29.4 us, 5.1 TB/s (some 3
-// us of it are the way to the first stage); 1 row, N = K = 4096, MXFP4: 6.4 us, of
+// us of it are the way to the first stage); 1 row, N = K = 4096, MXFP4: 5.8 us, of
 // which the weights need 1.4 and the way through launch, first stage and the
 // cluster's meeting the rest.
 //
@@ -370,26 +370,54 @@ moe_status_t matmul_error_word(const char *fn, MatmulErr *out) {
 }
 
 template <int WF, int NT, bool SPLIT>
+cudaLaunchConfig_t matmul_config(int items, int rank_log, cudaLaunchAttribute (&attr)[2], cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)items << rank_log);
+  cfg.blockDim = dim3(kMmThreads);
+  cfg.dynamicSmemBytes = MmGeom<WF, NT, SPLIT>::SMEM;
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1u << rank_log;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = SPLIT ? attr : attr + 1;
+  cfg.numAttrs = SPLIT ? 2 : 1;
+  return cfg;
+}
+
+// Clusters of 2^rank_log CTAs of the split kernel that run at once: fewer than the
+// SMs have room for, since a cluster stays within a GPC.  Asked once a device.
+template <int WF>
+int resident_clusters(int rank_log) {
+  using Geo = MmGeom<WF, 16, true>;
+  auto fn = fp4_matmul_kernel<WF, 16, true>;
+  static std::atomic<int> known[64][4];
+  static std::atomic<uint64_t> asked{0};
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if ((n = known[dev][rank_log].load(std::memory_order_relaxed))) return n - 1;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = matmul_config<WF, 16, true>(1, rank_log, attr, nullptr);
+  cfg.numAttrs = 1;                                        // the cluster alone
+  if (ask_shared(fn, Geo::SMEM, asked) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  known[dev][rank_log].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+template <int WF, int NT, bool SPLIT>
 cudaError_t launch_matmul(const MatmulArgs &a, int items, cudaStream_t s) {
   using Geo = MmGeom<WF, NT, SPLIT>;
   auto fn = fp4_matmul_kernel<WF, NT, SPLIT>;
   static std::atomic<uint64_t> asked{0};
   const cudaError_t e = ask_shared(fn, Geo::SMEM, asked);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)items << a.rank_log);
-  cfg.blockDim = dim3(kMmThreads);
-  cfg.dynamicSmemBytes = Geo::SMEM;
-  cfg.stream = s;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 1u << a.rank_log;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = SPLIT ? 2 : 1;
+  const cudaLaunchConfig_t cfg = matmul_config<WF, NT, SPLIT>(items, a.rank_log, attr, s);
   return cudaLaunchKernelEx(&cfg, fn, a);
 }
 
@@ -423,12 +451,17 @@ extern "C" moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_
   auto enc = map_encoder();
   if (!enc) return ops_fail(MOE_ERR_CUDA, fn, "cuTensorMapEncodeTiled is unavailable");
   // Which kernel, by the rows a group has on average and the blocks of 128 weight
-  // rows that can be in use (graph-timed us, N = K = 2048, NVFP4, unless said):
+  // rows that can be in use (graph-timed us, NVFP4, N = K = 2048 unless said):
   //  * up to 32 rows and blocks for every SM: weights are streamed, one CTA a block
   //    with token tiles of 32 (64 groups: 29.9 at 8 rows a group and 31.2 at 20;
   //    pairs 35.3 and 36.0; 38.0 and 37.7 at 40);
-  //  * up to 16 rows and fewer blocks: K split over clusters, tiles of 16 (dense, 1
-  //    row, N 4096: 5.7; unsplit 6.8, tiles of 32 6.3, pairs 7.0);
+  //  * items of 16 rows x 128 weight rows so few that clusters of 2, 4 or 8 SMs can
+  //    share each one's K, and the largest cluster with which all run at once (dense,
+  //    16 rows: 4 ways 5.7, 2 ways 6.7, unsplit 8.3, pairs 7.3; 8 ways, of which one
+  //    cluster waits for the others: 10.1; 64 rows, N 512, K 4096: 6.4, pairs 10.1).
+  //    Not for little K where it is cut in two or four and the tiles are full (K 512,
+  //    16 rows, N 8192: 5.8, pairs 5.4), nor unsplit but for single rows (K 512,
+  //    N 8192: 4.7, pairs 5.1; with 8 rows 5.5 and 5.2);
   //  * else pairs (dense, 64 rows, N 4096: 7.9, one CTA a block 10.2; 128 rows a
   //    group, 64 groups: 46; 92).
   const int sms = sm_count();
@@ -437,7 +470,19 @@ extern "C" moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_
   auto tiles = [&](int64_t nt) {
     return offsets ? std::min<int64_t>(rows, rows / nt + n_groups) : (rows + nt - 1) / nt;
   };
-  const bool streamed = mean <= 32 && blocks >= sms, split = !streamed && mean <= 16;
+  const bool mx = fmt == MOE_FMT_MXFP4;
+  const int nk = (K + 255) / 256;
+  const bool streamed = mean <= 32 && blocks >= sms;
+  bool split = false;
+  if (const int64_t items = tiles(16) * ((N + 127) / 128); !streamed && items <= sms) {
+    // one row of one or two stages: the meeting costs what the cut saves (4.2; 4.4)
+    const int most = nk > 2 || mean > 1 ? 3 : 0;
+    while (a.rank_log < most && items << (a.rank_log + 1) <= sms &&
+           items <= (mx ? resident_clusters<WF_MX>(a.rank_log + 1) : resident_clusters<WF_NV>(a.rank_log + 1)))
+      ++a.rank_log;
+    split = a.rank_log ? mean <= 8 || nk << a.rank_log >= 8 : mean == 1;
+    if (!split) a.rank_log = 0;
+  }
   // pairs: the smallest tile whose items still run at once, for its shorter
   // epilogue; else the largest, which moves the least
   const int64_t wide_blocks = (N + 255) / 256;
@@ -484,19 +529,13 @@ extern "C" moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_
   a.dtype = dtype;
   a.sf_wide = a.nsf % 16 == 0 && aligned_to(x_scales, 16) && aligned_to(w_scales, 16);
   a.y_vec = row_alignment(y, ldy * dtype_bytes(dtype)) >= 16;
-  const bool mx = fmt == MOE_FMT_MXFP4;
   cudaError_t e;
   if (streamed) {
     const int grid = (int)std::min<int64_t>(tiles(32) * ((N + 127) / 128), sms);
     e = mx ? launch_matmul<WF_MX, 32, false>(a, grid, s) : launch_matmul<WF_NV, 32, false>(a, grid, s);
   } else if (split) {
-    // one item a cluster; as many ways as keep every cluster resident (a second
-    // round doubles the time) and leave each way a step of the scales (four stages
-    // of MXFP4, two of NVFP4: four)
-    const int64_t items = tiles(16) * ((N + 127) / 128);
-    const int nk = (K + 255) / 256;
-    while (a.rank_log < 3 && items << (a.rank_log + 1) <= sms && nk >= 4 << a.rank_log) ++a.rank_log;
-    e = mx ? launch_matmul<WF_MX, 16, true>(a, (int)items, s) : launch_matmul<WF_NV, 16, true>(a, (int)items, s);
+    const int items = (int)(tiles(16) * ((N + 127) / 128));  // one a cluster
+    e = mx ? launch_matmul<WF_MX, 16, true>(a, items, s) : launch_matmul<WF_NV, 16, true>(a, items, s);
   } else {
     const int pairs = (int)std::min<int64_t>(tiles(nt) * wide_blocks, sms / 2);
     e = launch_matmul_pair(mx ? WF_MX : WF_NV, a, pairs, s);

@@ -442,6 +442,31 @@ def test_product_of_many_rows(fmt, lens, behind, N, K):
         assert t.equal(y, again)
 
 
+SHARED = [  # K shared by clusters of 8, 4 and 2, some with nothing to do, and the sizes beside them
+    ([16], 0, 128, 256), ([2], 0, 64, 32), ([16], 0, 1920, 2048), ([16], 0, 2048, 2048), ([64], 0, 500, 4096),
+    ([17], 0, 1024, 8192), ([200], 0, 100, 4064), ([1], 0, 2048, 4096), ([150], 0, 1024, 2048), ([130], 0, 1024, 1024),
+    ([33], 0, 10000, 288), ([16], 0, 16384, 512), ([8], 0, 8192, 512), ([1], 0, 8192, 256), ([1], 0, 128, 768),
+    ([40, 5, 33], 2, 300, 2304), ([0, 100, 0, 0, 17], 1, 130, 4608), ([1] * 9, 0, 1000, 544),
+]
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("lens, behind, N, K", SHARED)
+def test_product_whose_k_is_shared(fmt, lens, behind, N, K):
+    t, F = G.torch(), G.library()
+    rows, E = sum(lens) + behind, len(lens)
+    x, w = _operands(fmt, rows, E, N, K, rows + N + K)
+    off = None if E == 1 else t.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=t.int32, device="cuda")
+    for out, pad, shift in (("f32", 0, 0), ("bf16", 3, 1)):
+        y0 = placed(randn((rows, N), 1, out), pad, shift)
+        y = placed(y0, pad, shift)
+        F.fp4_matmul(x, w, off, out=y)
+        _check_product(x, w, off, y0, y, out)
+        again = placed(y0, pad, shift)
+        F.fp4_matmul(x, w, off, out=again)
+        assert t.equal(y, again)
+
+
 def test_grouped_product_of_a_first_row_past_zero():
     """offsets[0] > 0: the rows before the first segment stay as they are too."""
     t, F = G.torch(), G.library()
