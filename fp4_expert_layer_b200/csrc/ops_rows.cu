@@ -14,23 +14,27 @@
 // 48.7 us (94%), its backward 48.7 (95%), combine 48.9 (94%), its backward 97.8
 // (89%); 33 tokens 2.2 to 3.0 us.  More rows in flight a warp (8, or wider columns)
 // cost registers and with them warps: 59 to 74 us for combine.
+#include <type_traits>
+
 #include "ops_common.cuh"
 
 namespace moe {
 namespace {
 
-// A warp's 256 columns of one row, eight to a lane.  VEC: each lane has eight
-// consecutive ones and rows are 16-byte aligned; else lane l has columns
-// l, l + 32, ..., so that narrow accesses still coalesce.
+// A warp's 256 columns of one row, eight to a lane, moved N at a time: 8 where rows
+// start on 16 bytes, 2 where rows start and end on pairs, else 1 (lane l then has
+// columns N l ..., N (l + 32) ..., so that narrow accesses still coalesce).
 constexpr int kCols = 256;
 
 // STREAM: the rows are read once and the results written once, and take no place in
 // the caches that others would use.
-template <typename T, bool VEC, bool STREAM = false>
+template <typename T, int N, bool STREAM = false>
 struct Lane8 {
-  alignas(16) typename T::raw v[8];
-  __device__ __forceinline__ void load(const typename T::raw *row, int c0, int H, int lane) {
-    if constexpr (VEC) {
+  using raw = typename T::raw;
+  using pair = std::conditional_t<sizeof(raw) == 2, uint32_t, uint2>;
+  alignas(16) raw v[8];
+  __device__ __forceinline__ void load(const raw *row, int c0, int H, int lane) {
+    if constexpr (N == 8) {
       const int c = c0 + 8 * lane;
       if (c + 8 <= H) {
         uint4 *w = reinterpret_cast<uint4 *>(v);
@@ -39,18 +43,24 @@ struct Lane8 {
         for (int i = 0; i < (int)(sizeof(v) / 16); ++i) w[i] = STREAM ? __ldcs(p + i) : __ldg(p + i);
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c + i < H ? __ldg(row + c + i) : typename T::raw(0);
+        for (int i = 0; i < 8; ++i) v[i] = c + i < H ? __ldg(row + c + i) : raw(0);
+      }
+    } else if constexpr (N == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = c0 + 64 * i + 2 * lane;
+        reinterpret_cast<pair *>(v)[i] = c < H ? __ldg(reinterpret_cast<const pair *>(row + c)) : pair{};
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int c = c0 + 32 * i + lane;
-        v[i] = c < H ? __ldg(row + c) : typename T::raw(0);
+        v[i] = c < H ? __ldg(row + c) : raw(0);
       }
     }
   }
-  __device__ __forceinline__ void store(typename T::raw *row, int c0, int H, int lane) const {
-    if constexpr (VEC) {
+  __device__ __forceinline__ void store(raw *row, int c0, int H, int lane) const {
+    if constexpr (N == 8) {
       const int c = c0 + 8 * lane;
       if (c + 8 <= H) {
         const uint4 *w = reinterpret_cast<const uint4 *>(v);
@@ -64,6 +74,12 @@ struct Lane8 {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (c + i < H) row[c + i] = v[i];
+      }
+    } else if constexpr (N == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = c0 + 64 * i + 2 * lane;
+        if (c < H) *reinterpret_cast<pair *>(row + c) = reinterpret_cast<const pair *>(v)[i];
       }
     } else {
 #pragma unroll
@@ -137,7 +153,7 @@ struct CombineOpArgs {
 // A warp sums 256 columns of one token over its pairs.  The rows of four pairs
 // are loaded before the first is used.  (As streams 48.9 us of 8192 x 8, H 2048, bf16,
 // else 51.8; the backward pass loses by it, 105 and 98.)
-template <typename TI, typename TO, bool VEC>
+template <typename TI, typename TO, int N>
 __global__ void __launch_bounds__(128) combine_op_kernel(const CombineOpArgs a) {
   const int lane = threadIdx.x & 31;
   wait_prior_grid();
@@ -153,7 +169,7 @@ __global__ void __launch_bounds__(128) combine_op_kernel(const CombineOpArgs a) 
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
     for (int j0 = 0; j0 < a.k; j0 += 4) {
-      Lane8<TI, VEC, true> v[4];
+      Lane8<TI, N, true> v[4];
       int r[4];
       float g[4];
 #pragma unroll
@@ -170,7 +186,7 @@ __global__ void __launch_bounds__(128) combine_op_kernel(const CombineOpArgs a) 
         for (int i = 0; i < 8; ++i) acc[i] = fmaf(g[u], v[u].get(i), acc[i]);
       }
     }
-    Lane8<TO, VEC, true> out;
+    Lane8<TO, N, true> out;
 #pragma unroll
     for (int i = 0; i < 8; ++i) out.set(i, acc[i]);
     out.store(y + t * a.ldy, c0, a.H, lane);
@@ -178,11 +194,11 @@ __global__ void __launch_bounds__(128) combine_op_kernel(const CombineOpArgs a) 
 }
 
 template <typename TI, typename TO>
-cudaError_t launch_combine_op(CombineOpArgs a, bool vec, cudaStream_t s) {
+cudaError_t launch_combine_op(CombineOpArgs a, int n, cudaStream_t s) {
   a.chunks = (a.H + kCols - 1) / kCols;
   const long long blocks = std::min<long long>(((long long)a.T * a.chunks + 3) / 4, 1 << 20);
-  return launch_op(vec ? combine_op_kernel<TI, TO, true> : combine_op_kernel<TI, TO, false>, dim3((unsigned)blocks),
-                   128, 0, s, a);
+  auto fn = n == 8 ? combine_op_kernel<TI, TO, 8> : n == 2 ? combine_op_kernel<TI, TO, 2> : combine_op_kernel<TI, TO, 1>;
+  return launch_op(fn, dim3((unsigned)blocks), 128, 0, s, a);
 }
 
 // ---------------------------------------------------------- combine backward
@@ -199,7 +215,7 @@ struct CombineBwdArgs {
 // A CTA takes one token and `pairs` of its pairs; its warps take the 256-column
 // chunks in turn.  A warp keeps its chunk of dy in registers over the token's pairs: the pair's row of ys
 // gives a partial of its gate's gradient, gate * dy goes out as its row of dys.
-template <typename TD, typename TS, bool VEC>
+template <typename TD, typename TS, int N>
 __global__ void __launch_bounds__(256) combine_bwd_kernel(const CombineBwdArgs a) {
   __shared__ float part[8][kMaxTopK];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
@@ -214,10 +230,10 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const CombineBwdArgs a
     float mine = 0.0f;                                  // lane j: this warp's part of pair j's dot product
     for (int c = warp; c < a.chunks; c += W) {
       const int c0 = c * kCols;
-      Lane8<TD, VEC> d;
+      Lane8<TD, N> d;
       d.load(dy + t * a.lddy, c0, a.H, lane);
       for (int j0 = jb; j0 < je; j0 += 4) {
-        Lane8<TS, VEC> v[4];
+        Lane8<TS, N> v[4];
         int r[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -238,7 +254,7 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const CombineBwdArgs a
             if (lane == j0 + u) mine += s;
           }
           if (dys) {
-            Lane8<TS, VEC> out;
+            Lane8<TS, N> out;
 #pragma unroll
             for (int i = 0; i < 8; ++i) out.set(i, g * d.get(i));
             out.store(dys + (int64_t)r[u] * a.lddys, c0, a.H, lane);
@@ -260,7 +276,7 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const CombineBwdArgs a
 }
 
 template <typename TD, typename TS>
-cudaError_t launch_combine_bwd(CombineBwdArgs a, bool vec, cudaStream_t s) {
+cudaError_t launch_combine_bwd(CombineBwdArgs a, int n, cudaStream_t s) {
   a.chunks = (a.H + kCols - 1) / kCols;
   // eight warps to a token while tokens are few; once they fill the GPU four leave
   // fewer waits at the barrier (8192 tokens x 8, H 2048, bf16: 104 us with 8, 98
@@ -270,7 +286,8 @@ cudaError_t launch_combine_bwd(CombineBwdArgs a, bool vec, cudaStream_t s) {
   // with all pairs to a CTA 4.2)
   a.pairs = a.T < sm_count() ? 4 : a.k;
   const dim3 grid((unsigned)std::min(a.T, 1 << 20), (unsigned)((a.k + a.pairs - 1) / a.pairs));
-  return launch_op(vec ? combine_bwd_kernel<TD, TS, true> : combine_bwd_kernel<TD, TS, false>, grid, 32 * W, 0, s, a);
+  auto fn = n == 8 ? combine_bwd_kernel<TD, TS, 8> : n == 2 ? combine_bwd_kernel<TD, TS, 2> : combine_bwd_kernel<TD, TS, 1>;
+  return launch_op(fn, grid, 32 * W, 0, s, a);
 }
 
 // ------------------------------------------------------------ argument checks
@@ -281,7 +298,12 @@ moe_status_t check_shape(const char *fn, int32_t T, int32_t k, int32_t H, int32_
   return MOE_OK;
 }
 
-bool vec_rows(const void *p, int64_t ld, int32_t dt) { return !p || row_alignment(p, ld * dtype_bytes(dt)) >= 16; }
+// How many elements an access may take where rows of H start at p and every ld.
+int at_a_time(const void *p, int64_t ld, int32_t dt, int32_t H) {
+  if (!p) return 8;
+  const int es = dtype_bytes(dt), al = row_alignment(p, ld * es);
+  return al >= 16 ? 8 : al >= 2 * es && H % 2 == 0 ? 2 : 1;
+}
 
 }  // namespace
 }  // namespace moe
@@ -331,12 +353,12 @@ static moe_status_t combine_rows(const char *fn, const void *ys, int32_t ti, int
   if (!aligned_to(ys, dtype_bytes(ti)) || !aligned_to(y, dtype_bytes(to)))
     return ops_invalid(fn, "rows and the output must be aligned to their type");
   CombineOpArgs a{ys, y, inv, gates, ldys, ldy, T, k, rows, H, 0};
-  const bool vec = vec_rows(ys, ldys, ti) && vec_rows(y, ldy, to);
+  const int n = std::min(at_a_time(ys, ldys, ti, H), at_a_time(y, ldy, to, H));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
 #define MOE_CASE(I, TI) \
-  (to == MOE_DT_F32 ? launch_combine_op<TI, F32>(a, vec, s) : to == MOE_DT_BF16 ? launch_combine_op<TI, BF16>(a, vec, s) \
-                                                                                 : launch_combine_op<TI, F16>(a, vec, s))
+  (to == MOE_DT_F32 ? launch_combine_op<TI, F32>(a, n, s) : to == MOE_DT_BF16 ? launch_combine_op<TI, BF16>(a, n, s) \
+                                                                                 : launch_combine_op<TI, F16>(a, n, s))
   e = ti == MOE_DT_F32 ? MOE_CASE(0, F32) : ti == MOE_DT_BF16 ? MOE_CASE(1, BF16) : MOE_CASE(2, F16);
 #undef MOE_CASE
   return ops_launched(fn, e);
@@ -368,14 +390,14 @@ moe_status_t moe_combine_backward(const void *dy, int32_t dy_dtype, int64_t lddy
       !aligned_to(dys, dtype_bytes(ys_dtype)))
     return ops_invalid(fn, "dy, ys and dys must be aligned to their type");
   CombineBwdArgs a{dy, ys, dys, dgates, inv, gates, lddy, ldys, lddys, T, k, rows, H, 0, 0};
-  const bool vec = vec_rows(dy, lddy, dy_dtype) && (!dgates || vec_rows(ys, ldys, ys_dtype)) &&
-                   vec_rows(dys, lddys, ys_dtype);
+  const int n = std::min({at_a_time(dy, lddy, dy_dtype, H), dgates ? at_a_time(ys, ldys, ys_dtype, H) : 8,
+                          at_a_time(dys, lddys, ys_dtype, H)});
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
 #define MOE_CASE(TD)                                                                                       \
-  (ys_dtype == MOE_DT_F32 ? launch_combine_bwd<TD, F32>(a, vec, s)                                         \
-                          : ys_dtype == MOE_DT_BF16 ? launch_combine_bwd<TD, BF16>(a, vec, s)              \
-                                                    : launch_combine_bwd<TD, F16>(a, vec, s))
+  (ys_dtype == MOE_DT_F32 ? launch_combine_bwd<TD, F32>(a, n, s)                                         \
+                          : ys_dtype == MOE_DT_BF16 ? launch_combine_bwd<TD, BF16>(a, n, s)              \
+                                                    : launch_combine_bwd<TD, F16>(a, n, s))
   e = dy_dtype == MOE_DT_F32 ? MOE_CASE(F32) : dy_dtype == MOE_DT_BF16 ? MOE_CASE(BF16) : MOE_CASE(F16);
 #undef MOE_CASE
   return ops_launched(fn, e);

@@ -152,6 +152,20 @@ def test_combine_and_its_gradients(case, types):
     assert np.all(f64(dg)[iv < 0] == 0)
 
 
+EVEN = [  # T, k, E, sinks, H, pad, shift: rows that start and end on pairs, and some that do not quite
+    (11, 6, 16, 1, 2046, 0, 0), (9, 3, 8, 0, 258, 2, 2), (5, 8, 16, 0, 34, 0, 1), (4, 2, 4, 0, 256, 0, 2),
+    (6, 5, 8, 1, 254, 1, 0), (3, 1, 2, 0, 2, 0, 0), (200, 4, 16, 0, 98, 0, 2),
+]
+
+
+@pytest.mark.parametrize("types", [("bf16", "bf16"), ("f32", "bf16"), ("f32", "f32"), ("f16", "f32")])
+@pytest.mark.parametrize("case", EVEN)
+def test_rows_of_pairs(case, types):
+    test_combine_and_its_gradients(case, types)
+    test_dispatch_backward(case, types[0])
+    test_dispatch_copies_and_leaves_other_rows(case, types[0])
+
+
 def test_combine_gradient_against_differences():
     """Directional differences of <dy, combine(ys, gates)> in 64 bits."""
     F = G.library()
