@@ -29,7 +29,7 @@ EXPORTED = ["moe_layer_plan", "moe_admit", "moe_layer_create", "moe_set_slot_tab
             "moe_profile_enable", "moe_profile_read", "moe_route_topk_noalloc", "moe_debug_read",
             "moe_graph_capture", "moe_graph_launch", "moe_graph_destroy", "moe_set_policy", "moe_prefetch",
             "moe_fp4_quantize", "moe_fp4_dequantize", "moe_fp4_matmul", "moe_sort_tokens", "moe_dispatch",
-            "moe_dispatch_backward", "moe_combine", "moe_combine_backward"]
+            "moe_dispatch_backward", "moe_combine", "moe_combine_backward", "moe_debug_give_up"]
 POLICY = {"static": 0, "none": 1, "cache": 2, "hybrid": 3}
 
 
@@ -119,6 +119,7 @@ def lib():
         L.moe_fp4_quantize.argtypes = [p, i32, i64, i64, i64, i32, i64, p, p, p, p]
         L.moe_fp4_dequantize.argtypes = [p, p, p, i32, i64, i64, i64, p, i32, i64, p]
         L.moe_fp4_matmul.argtypes = [p, p, p, i32, p, p, p, i32, i32, i32, i32, p, p, i32, i64, p]
+        L.moe_debug_give_up.argtypes = [p]
         L.moe_sort_tokens.argtypes = [p, i32, i32, i32, p, p, p, p, p]
         L.moe_dispatch.argtypes = [p, i32, i32, i32, i32, i64, p, i32, p, i64, p]
         L.moe_dispatch_backward.argtypes = [p, i32, i32, i32, i32, i32, i64, p, p, i64, p]

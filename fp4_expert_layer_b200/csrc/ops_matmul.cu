@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
   __shared__ __align__(8) uint64_t acce_bar[NBUF];
   __shared__ __align__(8) uint64_t quiesce_bar;
   __shared__ uint32_t tmem_base_s;
+  __shared__ int gave_up;                                  // a wait of this CTA has
   __shared__ float xG_s[SPLIT ? NT : 1];
   __shared__ MmGroups groups;
 
@@ -87,7 +88,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
     mbar_fence_init();
   }
   if (tid == 32 * 2) {
-    mm_set_mirror(a);
+    gave_up = 0;
     tmap_prefetch(&a.wmap);
     tmap_prefetch(&a.xmap);
     for (int b = 0; b < NBUF; ++b) {
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
     bool failed = false;
     for (Walk m(a, groups, nrb, first, step); m.more() && !failed; m.next(a, groups)) {
       for (int it = k0; it < k1; ++it) {
-        if (issued >= S && !mbar_wait_warp(smem_u32(&empty_bar[s]), ph ^ 1u, a.err, 61)) { failed = true; break; }
+        if (issued >= S && !mm_wait_warp(smem_u32(&empty_bar[s]), ph ^ 1u, &gave_up, a.err, 61)) { failed = true; break; }
         const uint32_t bar = smem_u32(&full_bar[s]);
         const uint32_t st = smem_u32(smem + (size_t)s * Geo::STAGE);
         if (elect_one()) {
@@ -161,11 +162,11 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
     bool failed = false;
     for (Walk m(a, groups, nrb, first, step); m.more() && !failed; m.next(a, groups)) {
       const int buf = n % NBUF;
-      if (n >= NBUF && !mbar_wait_warp(smem_u32(&acce_bar[buf]), ((n / NBUF) - 1) & 1, a.err, 62)) break;
+      if (n >= NBUF && !mm_wait_warp(smem_u32(&acce_bar[buf]), ((n / NBUF) - 1) & 1, &gave_up, a.err, 62)) break;
       tc_fence_after();
       const uint32_t acc = tmem + (uint32_t)(buf * NT);
       for (int it = k0; it < k1; ++it) {
-        if (!mbar_wait_warp(smem_u32(&full_bar[s]), ph, a.err, 63)) { failed = true; break; }
+        if (!mm_wait_warp(smem_u32(&full_bar[s]), ph, &gave_up, a.err, 63)) { failed = true; break; }
         tc_fence_after();
         const uint32_t st = smem_u32(smem + (size_t)s * Geo::STAGE);
         const uint32_t sf_t = tmem + (uint32_t)(Geo::SF_TMEM + s * Geo::SF_COLS);
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
       int n = 0;
       for (Walk m(a, groups, nrb, first, step); m.more(); m.next(a, groups)) {
         const int buf = n % NBUF;
-        if (!mbar_wait_warp(smem_u32(&accf_bar[buf]), (n / NBUF) & 1, a.err, 64)) break;
+        if (!mm_wait_warp(smem_u32(&accf_bar[buf]), (n / NBUF) & 1, &gave_up, a.err, 64)) break;
         tc_fence_after();
         const uint32_t acc = tmem + (uint32_t)(buf * NT) + ((uint32_t)(32 * quad) << 16);
         const int col = m.rb * 128 + 32 * quad + lane;
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
           if (a.sf_wide) fetch_sf<WF, true>(a, rowp, tokens ? RG : 4, it0, k1, lo, hi, w);
           else fetch_sf<WF, false>(a, rowp, tokens ? RG : 4, it0, k1, lo, hi, w);
         },
-        [&](int s, uint32_t parity) { return mbar_wait_warp(smem_u32(&empty_bar[s]), parity, a.err, 65); },
+        [&](int s, uint32_t parity) { return mm_wait_warp(smem_u32(&empty_bar[s]), parity, &gave_up, a.err, 65); },
         [&](const Walk &) {
           return [&](int s, const uint32_t(&w)[4][8], int i) {
             const uint32_t dst = smem_u32(smem + (size_t)s * Geo::STAGE) + off;
@@ -276,7 +277,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
     bool ok = k1 > k0;                                     // a rank without stages adds nothing
     const float wG = (WF == WF_NV && any) ? __ldg(a.wG + m.g) : 1.0f;       // on their way while the products end
     if (WF == WF_NV && any && tid < m.nrows) xG_s[tid] = __ldg(a.xG + m.row0 + tid);
-    if (any && warp >= 2 && warp < 6) ok = mbar_wait_warp(smem_u32(&accf_bar[0]), 0, a.err, 66) && ok;
+    if (any && warp >= 2 && warp < 6) ok = mm_wait_warp(smem_u32(&accf_bar[0]), 0, &gave_up, a.err, 66) && ok;
     __syncwarp();
     cluster_wait();                                        // every rank has begun (long ago)
     const int plog = 7 - rlog, per = 1 << plog;
@@ -331,42 +332,71 @@ PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
   return fn;
 }
 
-// Error word of this device's products, in device memory (a poll of host memory
-// would put a PCIe round trip into a wait), and its mirror in mapped host memory,
-// which the next call reads.  Looked up and made once per device.
-__device__ ErrWord g_matmul_err;
-
-struct MatmulErr {
-  ErrWord *dev = nullptr;
-  int *host = nullptr;
+// Error word of each device's products, in mapped host memory: a wait that gives up
+// writes its code there, and the next call takes it.  Made by a device's first product,
+// also inside a stream capture, in which the allocation takes no part.
+struct MatmulErrors {
+  std::mutex mu;
+  int *word[64] = {};
 };
+MatmulErrors &matmul_errors() {
+  static MatmulErrors all;
+  return all;
+}
 
-moe_status_t matmul_error_word(const char *fn, MatmulErr *out) {
-  static std::mutex mu;
-  static MatmulErr words[64];
+moe_status_t matmul_error_word(const char *fn, int **out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || dev < 0 || dev >= 64) return ops_fail(MOE_ERR_CUDA, fn, "no current device");
-  std::lock_guard<std::mutex> lock(mu);
-  MatmulErr &w = words[dev];
-  if (!w.host) {
-    // also inside a stream capture: neither call takes part in it
+  MatmulErrors &all = matmul_errors();
+  std::lock_guard<std::mutex> lock(all.mu);
+  if (!all.word[dev]) {
     cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
     cudaThreadExchangeStreamCaptureMode(&mode);
-    void *d = nullptr, *h = nullptr;
-    e = cudaGetSymbolAddress(&d, g_matmul_err);
-    if (e == cudaSuccess) e = cudaHostAlloc(&h, sizeof(int), cudaHostAllocMapped | cudaHostAllocPortable);
+    void *h = nullptr;
+    e = cudaHostAlloc(&h, sizeof(int), cudaHostAllocMapped | cudaHostAllocPortable);
     cudaThreadExchangeStreamCaptureMode(&mode);
     if (e != cudaSuccess) {
       cudaGetLastError();
       return ops_fail(MOE_ERR_CUDA, fn, std::string("no error word: ") + cudaGetErrorString(e));
     }
-    w.dev = static_cast<ErrWord *>(d);
-    w.host = static_cast<int *>(h);
-    *w.host = 0;
+    *static_cast<int *>(h) = 0;
+    all.word[dev] = static_cast<int *>(h);
   }
-  *out = w;
+  *out = all.word[dev];
   return MOE_OK;
+}
+
+// Takes the failure that the current device's word holds, if any: read and cleared in
+// one step, so that one recorded meanwhile stays for the next call.
+moe_status_t matmul_take_error(const char *fn) {
+  int dev = 0, *word = nullptr;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return MOE_OK;
+  }
+  {
+    MatmulErrors &all = matmul_errors();
+    std::lock_guard<std::mutex> lock(all.mu);
+    word = all.word[dev];
+  }
+  if (!word || !*(volatile int *)word) return MOE_OK;
+  const int code = __atomic_exchange_n(word, 0, __ATOMIC_SEQ_CST);
+  if (!code) return MOE_OK;                                // another thread's call took it
+  return ops_fail(MOE_ERR_CUDA, fn, "a device-side wait of an earlier call gave up (code " + std::to_string(code) + ")");
+}
+
+// A wait that nothing ends, as the kernels wait, for a millisecond.
+__global__ void __launch_bounds__(32) give_up_kernel(int *err) {
+  __shared__ __align__(8) uint64_t bar;
+  __shared__ int gave_up;
+  if (threadIdx.x == 0) {
+    gave_up = 0;
+    mbar_init(smem_u32(&bar), 1);
+    mbar_fence_init();
+  }
+  __syncwarp();
+  mm_wait_warp(smem_u32(&bar), 0, &gave_up, err, 60, 1000000ull);
 }
 
 template <int WF, int NT, bool SPLIT>
@@ -439,6 +469,7 @@ extern "C" moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_
     return ops_invalid(fn, "need 1 <= n_groups <= 1024 and n_groups * N below 2^31");
   if (!offsets && n_groups != 1) return ops_invalid(fn, "more than one group needs offsets");
   if (ldy < N) return ops_invalid(fn, "ldy must be at least N");
+  if (const moe_status_t st = matmul_take_error(fn); st != MOE_OK) return st;
   if (rows == 0) return MOE_OK;
   if (!x_codes || !x_scales || !w_codes || !w_scales || !y) return ops_invalid(fn, "operands and y must be device pointers");
   if (fmt == MOE_FMT_NVFP4 && (!x_global || !w_global)) return ops_invalid(fn, "NVFP4 needs both global scales");
@@ -509,20 +540,11 @@ extern "C" moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_
       return ops_fail(MOE_ERR_CUDA, fn, "cuTensorMapEncodeTiled failed for w");
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  MatmulErr err;
-  const moe_status_t st = matmul_error_word(fn, &err);
-  if (st != MOE_OK) return st;
-  if (const int code = *(volatile int *)err.host) {
-    *(volatile int *)err.host = 0;
-    cudaMemsetAsync(&err.dev->code, 0, sizeof(int), s);
-    return ops_fail(MOE_ERR_CUDA, fn, "a device-side wait of an earlier call gave up (code " + std::to_string(code) + ")");
-  }
+  if (const moe_status_t st = matmul_error_word(fn, &a.err); st != MOE_OK) return st;
   a.xs = x_scales; a.ws = w_scales;
   a.xG = x_global; a.wG = w_global;
   a.offsets = offsets;
   a.y = y; a.ldy = ldy;
-  a.err = &err.dev->code;
-  a.err_host = err.host;
   a.rows = rows; a.groups = n_groups; a.N = N; a.K = K;
   while ((1 << a.tile_log) < nt) ++a.tile_log;
   a.nsf = K / (fmt == MOE_FMT_MXFP4 ? 32 : 16);
@@ -541,4 +563,12 @@ extern "C" moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_
     e = launch_matmul_pair(mx ? WF_MX : WF_NV, a, pairs, s);
   }
   return ops_launched(fn, e);
+}
+
+extern "C" moe_status_t moe_debug_give_up(void *stream) {
+  static const char fn[] = "moe_debug_give_up";
+  int *err = nullptr;
+  if (const moe_status_t st = matmul_error_word(fn, &err); st != MOE_OK) return st;
+  give_up_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(err);
+  return ops_launched(fn, cudaSuccess);
 }

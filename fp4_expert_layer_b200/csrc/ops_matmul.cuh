@@ -20,8 +20,7 @@ struct MatmulArgs {
   const int *offsets;            // NULL: one group of all rows
   void *y;
   int64_t ldy;
-  int *err;                      // the device's error word (an ErrWord), which the waits poll
-  int *err_host;                 // its mirror in mapped host memory
+  int *err;                      // the device's error word, in mapped host memory: written by waits that gave up
   int rows, groups, N, K;
   int tile_log;                  // a token tile has 2^tile_log rows
   int nsf;                       // scales in a row
@@ -31,9 +30,32 @@ struct MatmulArgs {
   int rank_log;                  // 2^rank_log CTAs of a cluster share an item's K
 };
 
-// The error word knows its mirror; every CTA says so before it waits for anything.
-__device__ __forceinline__ void mm_set_mirror(const MatmulArgs &a) {
-  reinterpret_cast<ErrWord *>(a.err)->host = a.err_host;
+// Bounded wait for phase `parity` of a barrier.  A wait that reaches its limit says so
+// in its CTA's flag, so that the CTA's other waits end too, and in the device's error
+// word, which the next call of the host reads.  Nothing that outlives the CTA is
+// polled: a launch that fails cannot end a wait of another launch, of its own next
+// replay, or of a CTA that works.
+__device__ __forceinline__ bool mm_wait(uint32_t bar, uint32_t parity, int *gave_up, int *err, int code,
+                                        unsigned long long limit = kWaitLimitNs) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = global_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 0) {
+      if (*(volatile int *)gave_up != 0) return false;
+      if (global_ns() - t0 > limit) {
+        *(volatile int *)gave_up = 1;
+        *(volatile int *)err = code;
+        __threadfence_system();
+        return false;
+      }
+    }
+  }
+}
+// The same by every lane of a warp, true only when it succeeded for all of them.
+__device__ __forceinline__ bool mm_wait_warp(uint32_t bar, uint32_t parity, int *gave_up, int *err, int code,
+                                             unsigned long long limit = kWaitLimitNs) {
+  return __all_sync(0xffffffffu, mm_wait(bar, parity, gave_up, err, code, limit));
 }
 
 // ------------------------------------------------------------------ work items

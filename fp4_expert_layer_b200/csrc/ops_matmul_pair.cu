@@ -68,6 +68,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
   __shared__ __align__(8) uint64_t free_bar;               // the even CTA's: the shared columns are read
   __shared__ __align__(8) uint64_t quiesce_bar;
   __shared__ uint32_t tmem_base_s;
+  __shared__ int gave_up;                                  // a wait of this CTA has
   __shared__ MmGroups groups;
 
   cg::cluster_group cluster = cg::this_cluster();
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
     mbar_fence_init();
   }
   if (tid == 32 * 2) {
-    mm_set_mirror(a);
+    gave_up = 0;
     tmap_prefetch(&a.wmap);
     tmap_prefetch(&a.xmap);
     mbar_init(smem_u32(&accf_bar[0]), 1);
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
       const int boxes = (half + kPairBox - 1) / kPairBox;
       const int wrow = m.rb * 256 + (int)rank * 128, xrow = m.row0 + (int)rank * half;
       for (int it = 0; it < nk; ++it) {
-        if (issued >= S && !mbar_wait_warp(smem_u32(&empty_bar[s]), ph ^ 1u, a.err, 71)) { failed = true; break; }
+        if (issued >= S && !mm_wait_warp(smem_u32(&empty_bar[s]), ph ^ 1u, &gave_up, a.err, 71)) { failed = true; break; }
         const uint32_t bar = cluster_addr(smem_u32(&full_bar[s]), 0);
         const uint32_t st = smem_u32(smem + (size_t)s * Geo::STAGE);
         if (elect_one()) {
@@ -154,10 +155,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
         m.next(a, groups);                                 // ahead of the waits
         const uint32_t id0 = idesc_fp4_block(256, cols, WF == WF_MX, 0, 0);
         const uint32_t id2 = idesc_fp4_block(256, cols, WF == WF_MX, 2, 2);
-        if (n > 0 && !mbar_wait_warp(smem_u32(&free_bar), (n - 1) & 1, a.err, 72)) break;
+        if (n > 0 && !mm_wait_warp(smem_u32(&free_bar), (n - 1) & 1, &gave_up, a.err, 72)) break;
         tc_fence_after();
         for (int it = 0; it < nk; ++it) {
-          if (!mbar_wait_warp(smem_u32(&full_bar[s]), ph, a.err, 73)) { failed = true; break; }
+          if (!mm_wait_warp(smem_u32(&full_bar[s]), ph, &gave_up, a.err, 73)) { failed = true; break; }
           tc_fence_after();
           const uint32_t st = smem_u32(smem + (size_t)s * Geo::STAGE);
           const uint32_t sf = tmem + (uint32_t)(Geo::SF_TMEM + turn * Geo::SF_COLS);
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
           xG[i] = 2 * i + odd < chunks && r < m.nrows ? wG * __ldg(a.xG + m.row0 + r) : 1.0f;
         }
       }
-      if (!mbar_wait_warp(smem_u32(&accf_bar[buf]), (n >> 1) & 1, a.err, 74)) break;
+      if (!mm_wait_warp(smem_u32(&accf_bar[buf]), (n >> 1) & 1, &gave_up, a.err, 74)) break;
       tc_fence_after();
       const uint32_t acc = tmem + (buf ? (uint32_t)(Geo::SF_TMEM - 32 * chunks) : 0u) + ((uint32_t)(32 * quad) << 16);
 
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
                           : a.xs + (size_t)min(m.row0 + 128 * (which - 1) + 32 * j + lane, a.rows - 1) * a.nsf;
         },
         [&](int it0, uint32_t(&w)[4][8]) { fetch_sf<WF, WIDE>(a, rowp, wanted ? 4 : 0, it0, nk, lo, hi, w); },
-        [&](int s, uint32_t parity) { return mbar_wait_warp(smem_u32(&empty_bar[s]), parity, a.err, 75); },
+        [&](int s, uint32_t parity) { return mm_wait_warp(smem_u32(&empty_bar[s]), parity, &gave_up, a.err, 75); },
         [&](const Walk &) {
           return [&, store = wanted](int s, const uint32_t(&w)[4][8], int i) {
             if (!store) return;

@@ -102,7 +102,9 @@ def fp4_matmul(x, w, offsets=None, out_dtype=torch.bfloat16, out=None, stream=No
     and per matrix of w).  ``offsets`` int32 [groups + 1] gives each group's rows
     (``sort_tokens`` writes it); without it w has one matrix and takes every row.
     Rows outside the groups are not written.  ``out`` takes the result in its own
-    type."""
+    type.  Should a bounded wait of a product have given up on the GPU, that
+    product's result is invalid, and the next call raises :class:`MoEError`, once
+    (a call with no rows asks, and enqueues nothing)."""
     if stream is None:
         got = _ops.fp4_matmul(x, w, offsets, out_dtype, out)
         if got is not None:

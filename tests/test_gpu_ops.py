@@ -841,3 +841,97 @@ def test_binding_refusals_on_the_gpu():
         with pytest.raises(F.MoEError) as ei:
             call()
         assert ei.value.status == 1, i
+
+
+# ------------------------------------------------- products after a wait that gave up
+def _give_up(F, stream=None):
+    s = G.torch().cuda.current_stream() if stream is None else stream
+    assert F.lib().moe_debug_give_up(s.cuda_stream) == 0
+
+
+def _reported_once(F, call):
+    with pytest.raises(F.MoEError) as ei:
+        call()
+    assert ei.value.status == 5 and "gave up" in str(ei.value)
+    return call()
+
+
+def _small_products():
+    """One of each kernel: K shared by a cluster, weights streamed, CTA pairs."""
+    t, F = G.torch(), G.library()
+    out = []
+    for i, (lens, N, K) in enumerate((([3], 256, 2048), ([2] * 80, 256, 256), ([300, 80], 512, 512))):
+        x, w = _operands("nvfp4", sum(lens), len(lens), N, K, 200 + i)
+        off = t.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=t.int32, device="cuda")
+        out.append((x, w, off, F.fp4_matmul(x, w, off)))
+    return out
+
+
+def test_a_wait_that_gave_up_is_reported_once():
+    t, F = G.torch(), G.library()
+    for x, w, off, want in _small_products():
+        _give_up(F)
+        t.cuda.synchronize()
+        y = t.full_like(want, 7.0)
+        with pytest.raises(F.MoEError) as ei:
+            F.fp4_matmul(x, w, off, out=y)
+        assert ei.value.status == 5 and "gave up" in str(ei.value)
+        t.cuda.synchronize()
+        assert (y == 7).all()                              # the refused call did nothing
+        assert t.equal(F.fp4_matmul(x, w, off), want)
+    for _ in range(2):                                     # two failures, one report
+        _give_up(F)
+    t.cuda.synchronize()
+    assert t.equal(_reported_once(F, lambda: F.fp4_matmul(x, w, off)), want)
+
+
+def test_a_failure_reported_inside_a_capture():
+    """The refused call adds no node; the capture goes on, and its replays are right."""
+    t, F = G.torch(), G.library()
+    for x, w, off, want in _small_products():
+        y = t.zeros_like(want)
+        _give_up(F)
+        t.cuda.synchronize()
+        g = t.cuda.CUDAGraph()
+        with t.cuda.graph(g):
+            _reported_once(F, lambda: F.fp4_matmul(x, w, off, out=y))
+        assert t.equal(F.fp4_matmul(x, w, off), want)      # before any replay
+        g.replay()
+        t.cuda.synchronize()
+        assert t.equal(y, want)
+
+
+def test_a_failure_ends_no_other_product():
+    """Products beside it on another stream, and replayed after it, are right."""
+    t, F = G.torch(), G.library()
+    side = t.cuda.Stream()
+    for x, w, off, want in _small_products():
+        y = t.zeros_like(want)
+        g = t.cuda.CUDAGraph()
+        with t.cuda.graph(g):
+            F.fp4_matmul(x, w, off, out=y)
+        t.cuda.synchronize()
+        _give_up(F, side)                                  # a millisecond on the side stream
+        for _ in range(3):                                 # the first replay beside it, the others after it
+            y.zero_()
+            g.replay()
+            t.cuda.synchronize()
+            assert t.equal(y, want)
+        with t.cuda.stream(side):
+            again = _reported_once(F, lambda: F.fp4_matmul(x, w, off))
+        t.cuda.synchronize()
+        assert t.equal(again, want)
+
+
+def test_a_program_that_only_replays_asks_with_no_rows():
+    t, F = G.torch(), G.library()
+    _, w, off, _ = _small_products()[2]
+    none = F.fp4_quantize(t.empty((0, 512), device="cuda"), "nvfp4")
+    assert F.fp4_matmul(none, w, off).shape == (0, 512)
+    g = t.cuda.CUDAGraph()
+    with t.cuda.graph(g):
+        _give_up(F)
+    for _ in range(2):
+        g.replay()
+        t.cuda.synchronize()
+        assert _reported_once(F, lambda: F.fp4_matmul(none, w, off)).shape == (0, 512)
