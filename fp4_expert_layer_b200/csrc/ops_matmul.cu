@@ -209,20 +209,27 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
       int n = 0;
       for (Walk m(a, groups, nrb, first, step); m.more(); m.next(a, groups)) {
         const int buf = n % NBUF;
+        float f = 1.0f;                                    // lane r: the factor of the item's row r
+        bool far = false;
+        const float wG = (WF == WF_NV) ? __ldg(a.wG + m.g) : 1.0f;
+        if constexpr (WF == WF_NV) {
+          static_assert(NT <= 32, "a row a lane");
+          if (lane < m.nrows) f = wG * __ldg(a.xG + m.row0 + lane);
+          far = !__all_sync(0xffffffffu, whole_factor(f));
+        }
         if (!mm_wait_warp(smem_u32(&accf_bar[buf]), (n / NBUF) & 1, &gave_up, a.err, 64)) break;
         tc_fence_after();
         const uint32_t acc = tmem + (uint32_t)(buf * NT) + ((uint32_t)(32 * quad) << 16);
         const int col = m.rb * 128 + 32 * quad + lane;
-        const float wG = (WF == WF_NV) ? __ldg(a.wG + m.g) : 1.0f;
+        if (far) store_far(a, acc, m.row0, m.nrows, col, wG);
 #pragma unroll 1
-        for (int c0 = 0; c0 < m.nrows; c0 += 16) {
+        for (int c0 = far ? m.nrows : 0; c0 < m.nrows; c0 += 16) {
           uint32_t d[16];
           tmem_ld16(acc + (uint32_t)c0, d);
-          const float xG = (WF == WF_NV && c0 + lane < m.nrows && lane < 16) ? __ldg(a.xG + m.row0 + c0 + lane) : 1.0f;
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float sc = (WF == WF_NV) ? wG * __shfl_sync(0xffffffffu, xG, j) : 1.0f;
+            const float sc = (WF == WF_NV) ? __shfl_sync(0xffffffffu, f, c0 + j) : 1.0f;
             if (c0 + j < m.nrows && col < a.N)
               store_out(a.y, a.dtype, (int64_t)(m.row0 + c0 + j) * a.ldy + col, __uint_as_float(d[j]) * sc);
           }
@@ -305,8 +312,11 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
         float v = 0.0f;
         for (int q = 0; q < ranks; ++q) v += recv[((size_t)q * per + r) * NT + c];
         const int col = m.rb * 128 + rank * per + r;
-        const float sc = (WF == WF_NV) ? wG * xG_s[c] : 1.0f;
-        if (col < a.N) store_out(a.y, a.dtype, (int64_t)(m.row0 + c) * a.ldy + col, v * sc);
+        if (WF == WF_NV) {
+          const float f = wG * xG_s[c];
+          v = whole_factor(f) ? v * f : scaled(v, xG_s[c], wG);
+        }
+        if (col < a.N) store_out(a.y, a.dtype, (int64_t)(m.row0 + c) * a.ldy + col, v);
       }
     }
   }

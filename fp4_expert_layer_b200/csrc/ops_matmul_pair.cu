@@ -214,6 +214,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
       // second, which shares its first ones, so those chunks go first
       auto chunk = [&](int i) { return buf ? i : chunks - 1 - i; };
       float xG[4];                                         // this warp's chunks' row scales times the matrix's
+      bool far = false;
       if constexpr (WF == WF_NV) {
         const float wG = __ldg(a.wG + m.g);
 #pragma unroll
@@ -221,10 +222,24 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
           const int r = 32 * chunk(2 * i + odd) + lane;
           xG[i] = 2 * i + odd < chunks && r < m.nrows ? wG * __ldg(a.xG + m.row0 + r) : 1.0f;
         }
+        far = !__all_sync(0xffffffffu, whole_factor(xG[0]) && whole_factor(xG[1]) && whole_factor(xG[2]) && whole_factor(xG[3]));
       }
       if (!mm_wait_warp(smem_u32(&accf_bar[buf]), (n >> 1) & 1, &gave_up, a.err, 74)) break;
       tc_fence_after();
       const uint32_t acc = tmem + (buf ? (uint32_t)(Geo::SF_TMEM - 32 * chunks) : 0u) + ((uint32_t)(32 * quad) << 16);
+      if constexpr (WF == WF_NV) {
+        if (far) {
+          const float wG = __ldg(a.wG + m.g);
+          for (int t = odd; t < chunks; t += 2) {
+            const int c = chunk(t);
+            store_far(a, acc + (uint32_t)(32 * c), m.row0 + 32 * c, min(32, m.nrows - 32 * c), col, wG);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(free_even);
+          continue;
+        }
+      }
 
       auto store = [&](const uint32_t (&d)[32], int c, float g) {
         const int have = min(32, m.nrows - 32 * c);

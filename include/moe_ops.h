@@ -67,7 +67,9 @@ moe_status_t moe_fp4_dequantize(const uint8_t *codes, const uint8_t *scales, con
 /* Grouped product of two FP4 operands on the block-scaled tensor cores:
  *   y[r, n] = xG[r] * wG[g] * sum_k x[r, k] * w[g, n, k]
  * for the rows r in [offsets[g], offsets[g + 1]) of each group g, accumulated in
- * fp32 and rounded once to dtype (F32, BF16 or F16).  x: codes and scales of
+ * fp32 and rounded once to dtype (F32, BF16 or F16).  The factor xG wG rounds to fp32
+ * first, and where it leaves fp32's normal numbers the scales meet the sum one by one,
+ * so that y has its value whenever y itself is in range.  x: codes and scales of
  * `rows` rows with one fp32 scale per row (rows_per_scale = 1); w: of n_groups
  * matrices of N rows with one fp32 scale per matrix (xG and wG NULL for MXFP4).
  * offsets: device int32 [n_groups + 1], non-decreasing (moe_sort_tokens writes

@@ -935,3 +935,54 @@ def test_a_program_that_only_replays_asks_with_no_rows():
         g.replay()
         t.cuda.synchronize()
         assert _reported_once(F, lambda: F.fp4_matmul(none, w, off)).shape == (0, 512)
+
+
+# ---------------------------------------------- global scales far from one another
+FAR = [  # x's scale, w's scale: their product leaves fp32's range, or its normal numbers, where y does not
+    (1.3 * 2.0 ** -70, 1.7 * 2.0 ** -75), (1.1 * 2.0 ** -75, 1.9 * 2.0 ** -80), (1.9 * 2.0 ** -66, 1.7 * 2.0 ** -62),
+    (-1.7 * 2.0 ** -90, 1.3 * 2.0 ** -50), (1.5 * 2.0 ** 60, 1.3 * 2.0 ** -140), (1.3 * 2.0 ** 100, 1.7 * 2.0 ** -120),
+]
+FAR_SIZES = [  # each kernel of the product: K shared, weights streamed, pairs with and without whole rows
+    ([3], 256, 2048, 0), ([20, 0, 13], 130, 512, 0), ([2] * 80, 256, 256, 0), ([300, 70], 512, 512, 0), ([300, 70], 515, 512, 1),
+]
+
+
+@pytest.mark.parametrize("lens, N, K, pad", FAR_SIZES)
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_global_scales_meet_the_sum_one_by_one(lens, N, K, pad, out):
+    t, F = G.torch(), G.library()
+    rows, E = sum(lens), len(lens)
+    x, w = _operands("nvfp4", rows, E, N, K, 300 + N)
+    rng = np.random.default_rng(N)
+    for q in (x, w):                                       # block scales up to the largest: sums near 2^25
+        q.scales.copy_(t.from_numpy(rng.integers(112, 127, tuple(q.scales.shape), dtype=np.uint8)))
+    off = t.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=t.int32, device="cuda")
+    for xg, wg in FAR:
+        far = t.arange(rows, device="cuda") % 3 != 1       # ordinary rows among them in every tile
+        x.global_scale.copy_(t.where(far, t.full((rows,), xg, device="cuda"), t.full((rows,), 2.0 ** -3 / abs(wg), device="cuda")
+                                     if 2.0 ** -3 / abs(wg) < 3e38 else t.full((rows,), 2.0 ** 100, device="cuda")))
+        w.global_scale.fill_(wg)
+        y = placed(t.zeros((rows, N), dtype=dt(out), device="cuda"), pad, pad)
+        F.fp4_matmul(x, w, off, out=y)
+        _check_product(x, w, off, t.zeros_like(y), y, out)
+
+
+@pytest.mark.parametrize("lens, N, K, pad", FAR_SIZES)
+def test_a_sum_of_zero_is_zero_at_any_global_scale(lens, N, K, pad):
+    """And a sum that is not stays infinite of its sign where the value passes the range."""
+    t, F = G.torch(), G.library()
+    rows, E = sum(lens), len(lens)
+    x, w = _operands("nvfp4", rows, E, N, K, 400 + N)
+    x.codes[::2] = 0
+    w.codes[:, 1::2] = 0
+    x.global_scale.fill_(2.0 ** 70)
+    w.global_scale.fill_(2.0 ** 80)
+    off = t.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=t.int32, device="cuda")
+    y = F.fp4_matmul(x, w, off, out_dtype=t.float32)
+    zero = t.zeros((rows, N), dtype=t.bool, device="cuda")
+    zero[::2] = True
+    zero[:, 1::2] = True
+    assert (y[zero] == 0).all()
+    one = x._replace(global_scale=t.ones_like(x.global_scale)), w._replace(global_scale=t.ones_like(w.global_scale))
+    sign = t.sign(F.fp4_matmul(*one, off, out_dtype=t.float32))
+    assert t.equal(y[sign != 0], sign[sign != 0] * float("inf"))
