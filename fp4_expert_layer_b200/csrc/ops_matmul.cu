@@ -473,8 +473,8 @@ extern "C" moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_
   static const char fn[] = "moe_fp4_matmul";
   if (fmt != MOE_FMT_MXFP4 && fmt != MOE_FMT_NVFP4) return ops_invalid(fn, "fmt must be MOE_FMT_MXFP4 or MOE_FMT_NVFP4");
   if (!is_float_dtype(dtype)) return ops_invalid(fn, "dtype must be F32, BF16 or F16");
-  if (rows < 0 || rows > kMmMaxRows || N < 1 || K < 32 || K % 32)
-    return ops_invalid(fn, "need 0 <= rows <= 2^27, N >= 1 and K a multiple of 32");
+  if (rows < 0 || rows > kMmMaxRows || N < 1 || N > kMmMaxSide || K < 32 || K % 32 || K > kMmMaxSide)
+    return ops_invalid(fn, "need 0 <= rows <= 2^27, 1 <= N <= 2^30 and K a multiple of 32, at most 2^30");
   if (n_groups < 1 || n_groups > kMmMaxGroups || (int64_t)n_groups * N >= (int64_t)1 << 31)
     return ops_invalid(fn, "need 1 <= n_groups <= 1024 and n_groups * N below 2^31");
   if (!offsets && n_groups != 1) return ops_invalid(fn, "more than one group needs offsets");

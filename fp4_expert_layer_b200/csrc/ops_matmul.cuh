@@ -12,6 +12,7 @@ namespace moe {
 
 constexpr int kMmMaxGroups = 1024;
 constexpr int kMmMaxRows = 1 << 27;   // the tile counts of 1024 groups then add up below 2^31
+constexpr int kMmMaxSide = 1 << 30;   // N and K: rounded up to tiles and stages they stay below 2^31
 
 struct MatmulArgs {
   CUtensorMap xmap, wmap;

@@ -79,7 +79,7 @@ moe_status_t moe_fp4_dequantize(const uint8_t *codes, const uint8_t *scales, con
  * Scale codes are read as in moe_admit: a NaN code makes its block NaN, NVFP4
  * scales must not be negative.
  * K is a multiple of 32, 1 <= n_groups <= 1024; codes are 16-byte aligned and y
- * aligned to its type; rows <= 2^27; N, K and n_groups * N below 2^31.  The scale rows
+ * aligned to its type; rows <= 2^27; N and K <= 2^30; n_groups * N below 2^31.  The scale rows
  * are read fastest when they start on 16 bytes (K a multiple of 512, with NVFP4 of
  * 256).  Every wait inside the kernel is bounded.  Should one give up, that launch's y
  * is invalid, and that launch's alone: whatever else is queued, runs beside it or

@@ -986,3 +986,21 @@ def test_a_sum_of_zero_is_zero_at_any_global_scale(lens, N, K, pad):
     one = x._replace(global_scale=t.ones_like(x.global_scale)), w._replace(global_scale=t.ones_like(w.global_scale))
     sign = t.sign(F.fp4_matmul(*one, off, out_dtype=t.float32))
     assert t.equal(y[sign != 0], sign[sign != 0] * float("inf"))
+
+
+@pytest.mark.parametrize("K", [1 << 30, (1 << 30) - 32])
+def test_product_of_the_longest_rows(K):
+    """Half a gigabyte of codes a row: what lies at the far end counts, and nothing twice."""
+    t, F = G.torch(), G.library()
+    codes = t.zeros((3, K // 2), dtype=t.uint8, device="cuda")
+    scales = t.full((3, K // 32), 127, dtype=t.uint8, device="cuda")
+    codes[0, -16:] = 0x22                                  # 32 ones in the last block
+    codes[0, 0] = 0x07                                     # and 6 in front
+    codes[1, -16:] = 0x44                                  # twos
+    codes[1, 0] = 0x02
+    codes[2, K // 4] = 0x22                                # elements that the row of x does not have
+    scales[0, -1] = 128
+    scales[1, -1] = 129
+    x = F.FP4Tensor(codes[:1], scales[:1], None, "mxfp4")
+    y = F.fp4_matmul(x, F.FP4Tensor(codes[1:], scales[1:], None, "mxfp4"), out_dtype=t.float32)
+    assert y.tolist() == [[6 + 32 * 2 * (2 * 4), 0]]

@@ -57,6 +57,17 @@ def test_matmul_refuses(F, bad):
     assert L.moe_last_error().startswith(b"moe_fp4_matmul")
 
 
+@pytest.mark.parametrize("bad", [
+    dict(N=(1 << 30) + 1, ldy=1 << 31), dict(N=(1 << 31) - 1, ldy=1 << 31), dict(K=(1 << 30) + 32),
+    dict(K=(1 << 31) - 224), dict(K=(1 << 31) - 32),
+])
+def test_matmul_refuses_sizes_whose_tile_counts_overflow(F, bad):
+    """One row, so that nothing else refuses them: a count of tiles or stages in 32 bits would be negative."""
+    L = F.lib()
+    assert L.moe_fp4_matmul(*_args(MATMUL, **dict(dict(rows=1, groups=1, N=1, ldy=1), **bad))) == 1
+    assert b"2^30" in L.moe_last_error()
+
+
 SORT = dict(ids=P, T=4, k=2, E=8, counts=P, offsets=P, perm=P, inv=P, stream=None)
 
 
