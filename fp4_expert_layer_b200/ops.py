@@ -87,7 +87,9 @@ def fp4_quantize(x, fmt="mxfp4", rows_per_scale=None, out=None, stream=None):
 
 
 def fp4_dequantize(q, dtype=torch.float32, out=None, stream=None):
-    """The values of an :class:`FP4Tensor`, rounded to ``dtype`` (float32 is exact)."""
+    """The values of an :class:`FP4Tensor`, each rounded once to ``dtype`` (float32 is
+    exact with a global scale of at most 18 digits, as :func:`fp4_quantize` makes them,
+    and within float32's range)."""
     if stream is None:
         got = _ops.fp4_dequantize(q, dtype, out)
         if got is not None:

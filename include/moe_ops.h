@@ -58,8 +58,11 @@ moe_status_t moe_fp4_quantize(const void *x, int32_t dtype, int64_t rows, int64_
                               int64_t rows_per_scale, uint8_t *codes, uint8_t *scales, float *global_scale,
                               void *stream);
 
-/* The values that codes stand for, rounded to dtype (F32, BF16 or F16; F32 is
- * exact).  Same shapes and limits as moe_fp4_quantize. */
+/* The values that codes stand for, code * scale * global_scale, each rounded once to
+ * dtype (F32, BF16 or F16), whatever fp32 number the global scale is.  F32 is exact
+ * where the value has an fp32 number: with MXFP4 up to its range (scale code 254 is
+ * 2^127, and 4 or 6 of it infinite), with NVFP4 where global_scale has at most 18 digits
+ * and the value is no subnormal.  Same shapes and limits as moe_fp4_quantize. */
 moe_status_t moe_fp4_dequantize(const uint8_t *codes, const uint8_t *scales, const float *global_scale, int32_t fmt,
                                 int64_t rows, int64_t K, int64_t rows_per_scale, void *out, int32_t dtype,
                                 int64_t ldo, void *stream);

@@ -1004,3 +1004,54 @@ def test_product_of_the_longest_rows(K):
     x = F.FP4Tensor(codes[:1], scales[:1], None, "mxfp4")
     y = F.fp4_matmul(x, F.FP4Tensor(codes[1:], scales[1:], None, "mxfp4"), out_dtype=t.float32)
     assert y.tolist() == [[6 + 32 * 2 * (2 * 4), 0]]
+
+
+# ------------------------------------------------ values at any global scale
+def _nearest(value, name):
+    """value (float64 products of a short number and an fp32 one: exact) rounded once to a type."""
+    t = G.torch()
+    f = t.finfo(dt(name))
+    m, e = np.frexp(value)
+    low = int(np.log2(f.smallest_normal)) + 1              # exponent (as frexp counts) of the smallest normal number
+    bits = int(round(-np.log2(f.eps))) + 1
+    step = np.ldexp(1.0, np.maximum(e, low) - bits)
+    r = np.round(value / step) * step                      # ties to even; the quotient is exact
+    return np.where(np.abs(r) > f.max, np.copysign(np.inf, r), r)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16", "f16"])
+def test_dequantize_rounds_once_at_any_global_scale(out):
+    """Every code and every scale code with global scales of 24 digits, from subnormal to near the end of the range."""
+    t, F = G.torch(), G.library()
+    rng = np.random.default_rng(7)
+    Gs = np.concatenate([rng.uniform(0.5, 2, 300), rng.uniform(0.5, 2, 300) * 2.0 ** rng.integers(-148, 127, 300),
+                         -rng.uniform(0.5, 2, 20), 2.0 ** rng.integers(-100, 100, 20), [0.0]]).astype(np.float32)
+    # a product that lies next to a border of bf16 or of f16: found by trying last digits
+    near = np.float32(1.5) + np.arange(64, dtype=np.float32) * np.float32(2.0 ** -23)
+    Gs = np.concatenate([Gs, near, near + np.float32(2.0 ** -8), near + np.float32(2.0 ** -11)])
+    n = Gs.size
+    codes = np.tile(np.arange(256, dtype=np.uint8), 127 * 8 // 256 + 1)[:127 * 8]
+    codes = np.stack([np.roll(codes, 3 * i) for i in range(n)])
+    codes = np.concatenate([codes, codes[:, :8]], 1)       # 128 blocks of 16: every finite scale, and 0 again
+    scales = np.tile(np.r_[np.arange(127), 0].astype(np.uint8), (n, 1))
+    scales[1::2] |= 128                                    # the entry point takes signs too
+    q = F.FP4Tensor(t.from_numpy(codes).cuda(), t.from_numpy(scales).cuda(), t.from_numpy(Gs).cuda(), "nvfp4")
+    want = _nearest(ref.values(codes, scales, Gs, "nvfp4"), out)
+    got = f64(F.fp4_dequantize(q, dtype=dt(out)))
+    bad = got != want
+    assert not bad.any(), f"{bad.sum()} of {bad.size}, first {got[bad][:4]} {want[bad][:4]}"
+    # one scale for all rows, of a tensor with three axes, into the caller's own rows
+    for g in Gs[[0, 301, 5]]:
+        one = F.FP4Tensor(q.codes.view(1, n, -1), q.scales.view(1, n, -1), t.tensor([g], device="cuda"), "nvfp4")
+        want = _nearest(ref.values(codes, scales, np.array([g]), "nvfp4", n), out)
+        assert np.array_equal(f64(F.fp4_dequantize(one, dtype=dt(out)))[0], want)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16", "f16"])
+def test_mxfp4_values_past_a_types_range(out):
+    """Scale code 254 is 2^127: 4 and 6 of it are infinite, as a rounding of any number past the range is."""
+    t, F = G.torch(), G.library()
+    codes = np.tile(np.arange(256, dtype=np.uint8), (255, 1))[:, :256]
+    scales = np.repeat(np.arange(255, dtype=np.uint8)[:, None], 512 // 32, axis=1)
+    q = F.FP4Tensor(t.from_numpy(codes).cuda(), t.from_numpy(scales).cuda(), None, "mxfp4")
+    assert np.array_equal(f64(F.fp4_dequantize(q, dtype=dt(out))), _nearest(ref.values(codes, scales, None, "mxfp4"), out))
