@@ -11,10 +11,12 @@ from __future__ import annotations
 import glob
 import importlib.util
 import os
+import runpy
 import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -23,6 +25,7 @@ INCLUDE = os.path.join(ROOT, "include")
 SO = os.path.join(HERE, "libfp4moe.so")
 SO_CHECKED = os.path.join(HERE, "libfp4moe_checked.so")
 SO_BINDING = os.path.join(HERE, "_ops.so")
+CUDA_ROOTS = (os.environ.get("CUDA_HOME"), os.environ.get("CUDA_PATH"), "/usr/local/cuda")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -47,20 +50,44 @@ def nvcc_cmd(out: str, extra=()):
              "--threads", "0", "-I", INCLUDE, "-I", CSRC, "-o", out] + list(extra) + sources())
 
 
+def _torch():
+    """(version, CUDA version or None, directory) of the installed torch, not imported; None without one."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return None
+    root = os.path.dirname(spec.origin)
+    v = runpy.run_path(os.path.join(root, "version.py"))
+    return v["__version__"], v.get("cuda"), root
+
+
+def _cuda_include():
+    """The CUDA toolkit's headers, of nvcc's toolkit or one at a usual place; None without one."""
+    nvcc = shutil.which("nvcc")
+    roots = [os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))] if nvcc else []
+    for root in roots + [r for r in CUDA_ROOTS if r]:
+        if os.path.exists(os.path.join(root, "include", "cuda_runtime_api.h")):
+            return os.path.join(root, "include")
+    return None
+
+
 def build_binding(force: bool = False) -> str | None:
-    """The operators' torch binding; None where torch is not installed."""
-    if importlib.util.find_spec("torch") is None:
+    """The operators' torch binding; None where there is no torch with CUDA, or no CUDA
+    toolkit to build it with (the library and the layer do without it)."""
+    torch = _torch()
+    if torch is None or torch[1] is None:
         return None
     src = os.path.join(CSRC, "ops_binding.cpp")
     deps = [src] + glob.glob(os.path.join(INCLUDE, "*.h"))
     if not force and os.path.exists(SO_BINDING) and all(os.path.getmtime(d) <= os.path.getmtime(SO_BINDING) for d in deps):
         return SO_BINDING
-    import torch
-    root = os.path.dirname(torch.__file__)
-    cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which("nvcc"))))
+    cuda = _cuda_include()
+    if cuda is None:
+        warnings.warn("the operators' torch binding is not built: no CUDA toolkit found (nvcc on the path, CUDA_HOME)")
+        return None
+    version, _, root = torch
     tmp = SO_BINDING + f".tmp{os.getpid()}"
-    subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f'-DMOE_TORCH_VERSION="{torch.__version__}"',
-                    "-I", INCLUDE, "-I", os.path.join(root, "include"), "-I", os.path.join(cuda, "include"),
+    subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f'-DMOE_TORCH_VERSION="{version}"',
+                    "-I", INCLUDE, "-I", os.path.join(root, "include"), "-I", cuda,
                     "-I", sysconfig.get_paths()["include"], src, "-o", tmp, "-L", os.path.join(root, "lib"),
                     "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"], check=True)
     os.replace(tmp, SO_BINDING)
@@ -68,14 +95,13 @@ def build_binding(force: bool = False) -> str | None:
 
 
 def build(force: bool = False, verbose: bool = False, checked: bool = False) -> str:
-    build_binding(force)
     so = SO_CHECKED if checked else SO
-    if not force and up_to_date(so):
-        return so
-    tmp = so + f".tmp{os.getpid()}"
-    extra = (["-Xptxas", "-v"] if verbose else []) + (["-DMOE_DEBUG_CHECKS"] if checked else [])
-    subprocess.run(nvcc_cmd(tmp, extra), check=True)
-    os.replace(tmp, so)
+    if force or not up_to_date(so):
+        tmp = so + f".tmp{os.getpid()}"
+        extra = (["-Xptxas", "-v"] if verbose else []) + (["-DMOE_DEBUG_CHECKS"] if checked else [])
+        subprocess.run(nvcc_cmd(tmp, extra), check=True)
+        os.replace(tmp, so)
+    build_binding(force)
     return so
 
 

@@ -153,3 +153,46 @@ def test_definition_of_a_tie():
     c, s, _, v = ref.quantize(x, "mxfp4")
     assert s[0, 0] == 127
     assert v[0, :16].tolist() == [6, 0, 1, 1, 2, 2, 4, 4, -0.0, -1, -1, -2, -2, -4, -4, 0]
+
+
+# ------------------------------------------------------------------ the build
+def _build_in_a_child(tmp_path, setup, path=()):
+    """What build.build() returns with the binding's file elsewhere; the library is up to date."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = f"from fp4_expert_layer_b200 import build as b\nb.SO_BINDING = {str(tmp_path / '_ops.so')!r}\n{setup}\nprint(b.build())"
+    env = {k: v for k, v in os.environ.items() if k not in ("CUDA_HOME", "CUDA_PATH")}
+    env["PYTHONPATH"] = os.pathsep.join([*map(str, path), root])
+    return subprocess.run([sys.executable, "-c", code], cwd=root, env=env, capture_output=True, text=True, timeout=600)
+
+
+def test_the_library_builds_beside_a_torch_without_cuda(F, tmp_path):
+    t = tmp_path / "torch"
+    t.mkdir()
+    for name in ("__init__.py", "version.py"):
+        (t / name).write_text("__version__ = '9.9.0+cpu'\ncuda = None\n")
+    r = _build_in_a_child(tmp_path, "", [tmp_path])
+    assert r.returncode == 0 and r.stdout.strip().endswith("libfp4moe.so"), r.stderr[-2000:]
+    assert not (tmp_path / "_ops.so").exists()
+
+
+def test_the_library_builds_where_the_binding_has_no_toolkit(F, tmp_path):
+    r = _build_in_a_child(tmp_path, "b.shutil.which = lambda name: None\nb.CUDA_ROOTS = ()")
+    assert r.returncode == 0 and r.stdout.strip().endswith("libfp4moe.so"), r.stderr[-2000:]
+    assert "binding is not built" in r.stderr and not (tmp_path / "_ops.so").exists()
+
+
+def test_a_binding_that_fails_to_compile_leaves_a_built_library(F, tmp_path):
+    """The library comes first, and the failure is not kept quiet."""
+    r = _build_in_a_child(tmp_path, "\n".join((
+        "import subprocess", "made = []",
+        "def run(cmd, check):",
+        "    made.append(cmd[0])",
+        "    if cmd[0] == 'g++': raise subprocess.CalledProcessError(1, cmd)",
+        "    open(cmd[cmd.index('-o') + 1], 'w').close()",
+        "b.subprocess.run = run", f"b.SO = {str(tmp_path / 'lib.so')!r}",
+        "import atexit; atexit.register(lambda: print(made))")))
+    assert r.returncode != 0 and "CalledProcessError" in r.stderr
+    assert "['nvcc', 'g++']" in r.stdout and (tmp_path / "lib.so").exists()
