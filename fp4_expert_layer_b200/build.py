@@ -78,8 +78,12 @@ def build_binding(force: bool = False) -> str | None:
         return None
     src = os.path.join(CSRC, "ops_binding.cpp")
     deps = [src] + glob.glob(os.path.join(INCLUDE, "*.h"))
-    if not force and os.path.exists(SO_BINDING) and all(os.path.getmtime(d) <= os.path.getmtime(SO_BINDING) for d in deps):
-        return SO_BINDING
+    key = f"{torch[0]} {sysconfig.get_config_var('SOABI')}\n"
+    stamp = os.path.splitext(SO_BINDING)[0] + ".stamp"     # the torch and the Python that the file is for
+    if not force and os.path.exists(SO_BINDING) and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read() == key and all(os.path.getmtime(d) <= os.path.getmtime(SO_BINDING) for d in deps):
+                return SO_BINDING
     cuda = _cuda_include()
     if cuda is None:
         warnings.warn("the operators' torch binding is not built: no CUDA toolkit found (nvcc on the path, CUDA_HOME)")
@@ -90,7 +94,11 @@ def build_binding(force: bool = False) -> str | None:
                     "-I", INCLUDE, "-I", os.path.join(root, "include"), "-I", cuda,
                     "-I", sysconfig.get_paths()["include"], src, "-o", tmp, "-L", os.path.join(root, "lib"),
                     "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"], check=True)
+    if os.path.exists(stamp):
+        os.remove(stamp)
     os.replace(tmp, SO_BINDING)
+    with open(stamp, "w") as f:
+        f.write(key)
     return SO_BINDING
 
 

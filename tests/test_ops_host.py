@@ -196,3 +196,28 @@ def test_a_binding_that_fails_to_compile_leaves_a_built_library(F, tmp_path):
         "import atexit; atexit.register(lambda: print(made))")))
     assert r.returncode != 0 and "CalledProcessError" in r.stderr
     assert "['nvcc', 'g++']" in r.stdout and (tmp_path / "lib.so").exists()
+
+
+def test_a_binding_of_another_torch_or_python_is_built_again(F, tmp_path, monkeypatch):
+    import os
+    from fp4_expert_layer_b200 import build as b
+    made = []
+
+    def compiled(cmd, check):
+        made.append(next(c for c in cmd if "MOE_TORCH_VERSION" in c))
+        open(cmd[cmd.index("-o") + 1], "w").close()
+
+    here = b._torch()
+    monkeypatch.setattr(b, "SO_BINDING", str(tmp_path / "_ops.so"))
+    monkeypatch.setattr(b.subprocess, "run", compiled)
+    assert b.build_binding() == b.SO_BINDING and b.build_binding() == b.SO_BINDING
+    assert len(made) == 1 and here[0] in made[0]
+    monkeypatch.setattr(b, "_torch", lambda: ("9.9.0", *here[1:]))
+    b.build_binding(), b.build_binding()
+    assert len(made) == 2 and "9.9.0" in made[1]
+    monkeypatch.setattr(b.sysconfig, "get_config_var", lambda name: "cpython-399")
+    b.build_binding(), b.build_binding()
+    assert len(made) == 3
+    os.remove(b.SO_BINDING)
+    b.build_binding()
+    assert len(made) == 4
