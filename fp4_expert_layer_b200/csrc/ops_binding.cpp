@@ -15,6 +15,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -129,6 +130,24 @@ PyObject *wrap(const Tensor &t) {
   return o;
 }
 PyObject *given(PyObject *o) { Py_INCREF(o); return o; }
+
+// What autograd has to know of a caller's tensor that is written past the dispatcher.  A
+// graph that records it would keep the old value's gradient: refused, as torch's own out=
+// is.  A graph that has saved it goes by its version.
+const Tensor &writable(const char *fn, const Tensor &out) {
+  if (c10::GradMode::is_enabled() && out.requires_grad())
+    bad("%s: out requires grad, and the write would not be in its graph (detach it, or call under torch.no_grad())", fn);
+  return out;
+}
+void written(const Tensor &out) {
+  if (!out.is_inference()) out.unsafeGetTensorImpl()->bump_version();
+}
+// The call's result: a new tensor, or the one that the caller gave.
+PyObject *handed(PyObject *out_o, const Tensor &out) {
+  if (out_o == Py_None) return wrap(out);
+  written(out);
+  return given(out_o);
+}
 
 int block_of(PyObject *fmt) {       // elements of a block, 0 if the format is unknown
   if (!PyUnicode_Check(fmt)) return 0;
@@ -248,13 +267,17 @@ PyObject *quantize(PyObject *const *a) {
     codes = *q.codes;
     scales = *q.scales;
     if (nv) {
-      G = *q.G;
+      G = writable(fn, *q.G);
       contiguous(fn, "out.global_scale", G, at::kFloat, {n / per});
     }
   }
   done(c_quantize(x.data_ptr(), type, n, K, ld, nv ? MOE_FMT_NVFP4 : MOE_FMT_MXFP4, per, ptr<uint8_t>(codes),
                   ptr<uint8_t>(scales), nv ? ptr<float>(G) : nullptr, stream_of(x)));
-  return a[3] == Py_None ? make_fp4(codes, scales, nv ? &G : nullptr, a[1]) : given(a[3]);
+  if (a[3] == Py_None) return make_fp4(codes, scales, nv ? &G : nullptr, a[1]);
+  written(codes);
+  written(scales);
+  if (nv) written(G);
+  return given(a[3]);
 }
 
 // (q, dtype, out | None)
@@ -280,7 +303,7 @@ PyObject *dequantize(PyObject *const *a) {
   if (a[2] == Py_None) {
     out = make(at::IntArrayRef(shape, dim), dtype_of(fn, a[1]), c);
   } else {
-    out = tensor(a[2], fn, "out");
+    out = writable(fn, tensor(a[2], fn, "out"));
     same(fn, c, "out", out);
     if (out.sizes() != at::IntArrayRef(shape, dim)) bad("%s: out is of another shape", fn);
     if (dim == 2) ld = row_stride(fn, "out", out);
@@ -288,7 +311,7 @@ PyObject *dequantize(PyObject *const *a) {
   }
   done(c_dequantize(q.c(), q.s(), q.g(), q.fmt, q.rows, q.K, per, out.data_ptr(), float_type(fn, "out", out), ld,
                     stream_of(c)));
-  return a[2] == Py_None ? wrap(out) : given(a[2]);
+  return handed(a[2], out);
 }
 
 // (x, w, offsets | None, out_dtype, out | None)
@@ -320,13 +343,13 @@ PyObject *matmul(PyObject *const *a) {
   if (a[4] == Py_None) {
     out = make({n, N}, dtype_of(fn, a[3]), xc);
   } else {
-    out = tensor(a[4], fn, "out");
+    out = writable(fn, tensor(a[4], fn, "out"));
     same(fn, xc, "out", out);
     if (out.dim() != 2 || out.size(0) != n || out.size(1) != N) bad("%s: out must be [%d, %d]", fn, n, N);
   }
   done(c_matmul(x.c(), x.s(), x.g(), n, w.c(), w.s(), w.g(), groups, N, K, x.fmt, offsets, out.data_ptr(),
                 float_type(fn, "out", out), row_stride(fn, "out", out), stream_of(xc)));
-  return a[4] == Py_None ? wrap(out) : given(a[4]);
+  return handed(a[4], out);
 }
 
 // ------------------------------------------------------------------ expert rows
@@ -380,13 +403,12 @@ Pairs pairs(const char *fn, const Tensor &first, PyObject *inv_o, PyObject *gate
 Tensor result(const char *fn, const Tensor &first, PyObject *out_o, int64_t n, int64_t cols, at::ScalarType type,
               bool typed) {
   if (out_o == Py_None) return make({n, cols}, type, first);
-  const Tensor &out = tensor(out_o, fn, "out");
+  const Tensor &out = writable(fn, tensor(out_o, fn, "out"));
   same(fn, first, "out", out);
   if (out.dim() != 2 || out.size(0) != n || out.size(1) != cols || (typed && out.scalar_type() != type))
     bad("%s: out must be %s [%lld, %lld]", fn, typed ? c10::toString(type) : "of a float type", (long long)n, (long long)cols);
   return out;
 }
-PyObject *handed(PyObject *out_o, const Tensor &out) { return out_o == Py_None ? wrap(out) : given(out_o); }
 
 // (x, inv, rows | None, out | None)
 PyObject *dispatch(PyObject *const *a) {

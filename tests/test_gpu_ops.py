@@ -1055,3 +1055,65 @@ def test_mxfp4_values_past_a_types_range(out):
     scales = np.repeat(np.arange(255, dtype=np.uint8)[:, None], 512 // 32, axis=1)
     q = F.FP4Tensor(t.from_numpy(codes).cuda(), t.from_numpy(scales).cuda(), None, "mxfp4")
     assert np.array_equal(f64(F.fp4_dequantize(q, dtype=dt(out))), _nearest(ref.values(codes, scales, None, "mxfp4"), out))
+
+
+# ------------------------------------------------------------- autograd's records
+def _writes():
+    """Each call that takes `out`: (call, outputs whose memory it writes)."""
+    t, F = G.torch(), G.library()
+    inv = t.arange(8, dtype=t.int32, device="cuda").view(4, 2)
+    x, ys, dy = randn((4, 64), 1), randn((8, 64), 2), randn((4, 64), 3)
+    xq, wq = _operands("nvfp4", 4, 1, 8, 64, 5)
+    q = F.FP4Tensor(t.empty_like(xq.codes), t.empty_like(xq.scales), t.empty_like(xq.global_scale), "nvfp4")
+    new = lambda *shape: t.zeros(shape, device="cuda")
+    return {
+        "fp4_quantize": (lambda out, **kw: F.fp4_quantize(x, "nvfp4", out=q, **kw), q[:3]),
+        "fp4_dequantize": (lambda out, **kw: F.fp4_dequantize(xq, out=out, **kw), [new(4, 64)]),
+        "fp4_matmul": (lambda out, **kw: F.fp4_matmul(xq, wq, out=out, **kw), [new(4, 8)]),
+        "dispatch": (lambda out, **kw: F.dispatch(x, inv, out=out, **kw), [new(8, 64)]),
+        "dispatch_backward": (lambda out, **kw: F.dispatch_backward(ys, inv, out=out, **kw), [new(4, 64)]),
+        "combine": (lambda out, **kw: F.combine(ys, inv, out=out, **kw), [new(4, 64)]),
+        "combine_backward": (lambda out, **kw: F.combine_backward(dy, ys, inv, out=out, **kw), [new(8, 64)]),
+    }
+
+
+@pytest.mark.parametrize("name", ["fp4_quantize", "fp4_dequantize", "fp4_matmul", "dispatch", "dispatch_backward", "combine",
+                                  "combine_backward"])
+def test_a_written_out_moves_its_version(name):
+    """What autograd goes by when a tensor that it saved has been overwritten."""
+    t = G.torch()
+    call, outs = _writes()[name]
+    before = [o._version for o in outs]
+    call(outs[0])
+    assert all(o._version > v for o, v in zip(outs, before))
+    middle = [o._version for o in outs]
+    call(outs[0], stream=t.cuda.current_stream())
+    assert all(o._version > v for o, v in zip(outs, middle))
+    if name != "fp4_quantize":                             # the squares' gradient needs the values that are gone
+        leaf = t.ones_like(outs[0], requires_grad=True)
+        loss = (leaf * outs[0]).sum()
+        call(outs[0])
+        with pytest.raises(RuntimeError, match="inplace"):
+            loss.backward()
+    with t.inference_mode():                               # tensors without a version are written as ever
+        call_in, outs_in = _writes()[name]
+        call_in(outs_in[0])
+    call_in(outs_in[0])
+
+
+@pytest.mark.parametrize("name", ["fp4_dequantize", "fp4_matmul", "dispatch", "dispatch_backward", "combine",
+                                  "combine_backward"])
+def test_an_out_that_records_a_graph_is_refused(name):
+    """As torch's own out= refuses it; not where nothing is recorded."""
+    t, F = G.torch(), G.library()
+    call, (out,) = _writes()[name]
+    leaf = out.requires_grad_()
+    for o in (leaf, leaf * 2):
+        kept = o.detach().clone()
+        with pytest.raises(F.MoEError) as ei:
+            call(o)
+        assert ei.value.status == 1 and "out requires grad" in str(ei.value)
+        assert t.equal(o.detach(), kept)
+        with t.no_grad():
+            call(o)
+        assert not t.equal(o.detach(), kept)
