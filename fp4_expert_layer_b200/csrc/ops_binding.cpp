@@ -139,6 +139,15 @@ const Tensor &writable(const char *fn, const Tensor &out) {
     bad("%s: out requires grad, and the write would not be in its graph (detach it, or call under torch.no_grad())", fn);
   return out;
 }
+// An input whose gradient the caller may expect: the result is detached all the same.
+void detached(const char *fn, const char *name, const Tensor &t) {
+  if (!t.requires_grad() || !c10::GradMode::is_enabled()) return;
+  char text[256];
+  snprintf(text, sizeof text,
+           "%s: %s requires grad, but no graph is recorded: the gradients are calls of their own (detach it, or call "
+           "under torch.no_grad() or within a torch.autograd.Function)", fn, name);
+  if (PyErr_WarnEx(PyExc_UserWarning, text, 2) < 0) throw Refused{};
+}
 void written(const Tensor &out) {
   if (!out.is_inference()) out.unsafeGetTensorImpl()->bump_version();
 }
@@ -294,6 +303,7 @@ PyObject *dequantize(PyObject *const *a) {
     if (q.rows && (!groups || q.rows % groups))
       bad("%s: %lld global scales do not divide %lld rows", fn, (long long)groups, (long long)q.rows);
     per = std::max<int64_t>(1, q.rows / std::max<int64_t>(1, groups));
+    detached(fn, "q.global_scale", *q.G);
   }
   int64_t shape[4];
   for (int i = 0; i < dim; ++i) shape[i] = c.size(i);
@@ -329,6 +339,8 @@ PyObject *matmul(PyObject *const *a) {
   if (x.G) {
     contiguous(fn, "x.global_scale", *x.G, at::kFloat, {n});
     contiguous(fn, "w.global_scale", *w.G, at::kFloat, {groups});
+    detached(fn, "x.global_scale", *x.G);
+    detached(fn, "w.global_scale", *w.G);
   }
   const int32_t *offsets = nullptr;
   if (a[2] != Py_None) {
@@ -395,6 +407,7 @@ Pairs pairs(const char *fn, const Tensor &first, PyObject *inv_o, PyObject *gate
     const Tensor &g = tensor(gates_o, fn, "gates");
     contiguous(fn, "gates", g, at::kFloat, inv.sizes());
     same(fn, first, "gates", g);
+    detached(fn, "gates", g);
     p.gates = ptr<const float>(g);
   }
   return p;
@@ -416,6 +429,7 @@ PyObject *dispatch(PyObject *const *a) {
   const Tensor &x = tensor(a[0], fn, "x");
   if (!here(x)) Py_RETURN_NONE;
   two_axes(fn, "x", x);
+  detached(fn, "x", x);
   const int64_t H = x.size(1);
   const Pairs p = pairs(fn, x, a[1], nullptr, x.size(0));
   int64_t rows = (int64_t)p.T * p.k;
@@ -435,6 +449,7 @@ PyObject *dispatch_backward(PyObject *const *a) {
   const Tensor &d = tensor(a[0], fn, "dxs");
   if (!here(d)) Py_RETURN_NONE;
   two_axes(fn, "dxs", d);
+  detached(fn, "dxs", d);
   const int32_t rows = size32(fn, "rows", d.size(0)), H = size32(fn, "H", d.size(1)), type = float_type(fn, "dxs", d);
   const Pairs p = pairs(fn, d, a[1], nullptr, -1);
   const Tensor out = result(fn, d, a[2], p.T, H, d.scalar_type(), true);
@@ -449,6 +464,7 @@ PyObject *combine(PyObject *const *a) {
   const Tensor &ys = tensor(a[0], fn, "ys");
   if (!here(ys)) Py_RETURN_NONE;
   two_axes(fn, "ys", ys);
+  detached(fn, "ys", ys);
   const int32_t rows = size32(fn, "rows", ys.size(0)), H = size32(fn, "H", ys.size(1)), type = float_type(fn, "ys", ys);
   const Pairs p = pairs(fn, ys, a[1], a[2], -1);
   const at::ScalarType want = a[3] == Py_None ? ys.scalar_type() : dtype_of(fn, a[3]);
@@ -467,6 +483,8 @@ PyObject *combine_backward(PyObject *const *a) {
   two_axes(fn, "dy", dy);
   two_axes(fn, "ys", ys);
   same(fn, dy, "ys", ys);
+  detached(fn, "dy", dy);
+  detached(fn, "ys", ys);
   if (ys.size(1) != dy.size(1)) bad("%s: dy and ys have rows of %lld and %lld", fn, (long long)dy.size(1), (long long)ys.size(1));
   const int32_t rows = size32(fn, "rows", ys.size(0)), H = size32(fn, "H", ys.size(1));
   const int32_t td = float_type(fn, "dy", dy), ts = float_type(fn, "ys", ys);

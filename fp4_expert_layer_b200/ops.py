@@ -15,8 +15,10 @@ tensors' device (or on ``stream``) and returns; a refused argument raises
 :class:`MoEError`.  ``out`` takes the result in the caller's own tensor; rows
 that a call does not write (see the header) are then left as they were, and are
 uninitialised in a result that the call allocates.  The gradients are calls of
-their own: nothing here records an autograd graph.  So an ``out`` that requires
-grad is refused while grad mode is on; any other counts as modified in place.
+their own: nothing here records an autograd graph.  So while grad mode is on an
+``out`` that requires grad is refused, and an input that does (but for
+``fp4_quantize``, whose codes have no gradient) is warned of; any ``out`` counts
+as modified in place.
 """
 from __future__ import annotations
 

@@ -1117,3 +1117,86 @@ def test_an_out_that_records_a_graph_is_refused(name):
         with t.no_grad():
             call(o)
         assert not t.equal(o.detach(), kept)
+
+
+def _detached_calls():
+    """Each call whose result is a number times an input: (call, that input, the function's name)."""
+    t, F = G.torch(), G.library()
+    inv = t.arange(8, dtype=t.int32, device="cuda").view(4, 2)
+    x, ys, dy, gates = randn((4, 64), 1), randn((8, 64), 2), randn((4, 64), 3), randn((4, 2), 4)
+    xq, wq = _operands("nvfp4", 4, 1, 8, 64, 5)
+    scaled = lambda q: lambda g: q._replace(global_scale=g)
+    return [
+        (lambda v: F.dispatch(v, inv), x, "dispatch"), (lambda v: F.dispatch_backward(v, inv), ys, "dispatch_backward"),
+        (lambda v: F.combine(v, inv, gates), ys, "combine"), (lambda v: F.combine(ys, inv, v), gates, "combine"),
+        (lambda v: F.combine_backward(v, ys, inv, gates), dy, "combine_backward"),
+        (lambda v: F.combine_backward(dy, v, inv, gates), ys, "combine_backward"),
+        (lambda v: F.combine_backward(dy, ys, inv, v), gates, "combine_backward"),
+        (lambda v: F.fp4_dequantize(scaled(xq)(v)), xq.global_scale, "fp4_dequantize"),
+        (lambda v: F.fp4_matmul(scaled(xq)(v), wq), xq.global_scale, "fp4_matmul"),
+        (lambda v: F.fp4_matmul(xq, scaled(wq)(v)), wq.global_scale, "fp4_matmul"),
+    ]
+
+
+def test_an_input_whose_gradient_is_not_recorded_is_warned_of():
+    """The result is what it was, detached; no warning where nothing would be recorded anyway."""
+    import warnings
+    t, F = G.torch(), G.library()
+    first = lambda r: r[0] if isinstance(r, tuple) else r
+    for call, v, name in _detached_calls():
+        want = first(call(v))
+        leaf = v.clone().requires_grad_()
+        with pytest.warns(UserWarning, match=f"{name}: .* requires grad"):
+            got = first(call(leaf))
+        assert t.equal(got, want) and not got.requires_grad
+        with warnings.catch_warnings():
+            warnings.simplefilter("error")
+            with t.no_grad():
+                assert t.equal(first(call(leaf)), want)
+            assert t.equal(first(call(leaf.detach())), want)
+            with pytest.raises(UserWarning):               # a program may make errors of them
+                call(leaf)
+    with warnings.catch_warnings():                        # codes have no gradient: quantising a parameter is no mistake
+        warnings.simplefilter("error")
+        F.fp4_quantize(t.nn.Parameter(randn((8, 64), 6)), "nvfp4")
+
+
+def test_gradients_called_within_a_function_of_ones_own():
+    """combine and dispatch as torch.autograd.Functions: the calls inside them are not warned of."""
+    import warnings
+    t, F = G.torch(), G.library()
+    T, k, E, H = 9, 3, 5, 64
+    inv = _rows_case(T, k, E, 1, 7)["inv"]
+
+    class Dispatch(t.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            return F.dispatch(x, inv, out=x.new_zeros(T * k, H))
+
+        @staticmethod
+        def backward(ctx, d):
+            return F.dispatch_backward(d.contiguous(), inv)
+
+    class Combine(t.autograd.Function):
+        @staticmethod
+        def forward(ctx, ys, gates):
+            ctx.save_for_backward(ys, gates)
+            return F.combine(ys, inv, gates)
+
+        @staticmethod
+        def backward(ctx, d):
+            ys, gates = ctx.saved_tensors
+            return F.combine_backward(d.contiguous(), ys, inv, gates, out=t.zeros_like(ys))
+
+    x, gates, dy = randn((T, H), 8).requires_grad_(), randn((T, k), 9).requires_grad_(), randn((T, H), 10)
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        y = Combine.apply(Dispatch.apply(x).square(), gates)
+        y.backward(dy)
+    iv = inv.cpu().numpy()
+    xs = ref.dispatch(f64(x), iv, np.zeros((T * k, H)))
+    dys, dg, mag = ref.combine_backward(f64(dy), xs ** 2, iv, f64(gates), np.zeros((T * k, H)))
+    dx, dmag = ref.combine(2 * xs * dys, iv, np.ones((T, k)))
+    # three fp32 roundings of xs^2 and its gradient, and the sums' own
+    assert np.all(np.abs(f64(gates.grad) - dg) <= (H + 1) * 2.0 ** -24 * mag * (1 + 2.0 ** -20) + TINY["f32"])
+    assert np.all(np.abs(f64(x.grad) - dx) <= (k + 4) * 2.0 ** -24 * dmag * (1 + 2.0 ** -20) + TINY["f32"])
