@@ -53,9 +53,12 @@ _ops.setup(MoEError, FP4Tensor, *(C.cast(getattr(lib(), "moe_" + n), C.c_void_p)
     "combine_backward", "last_error")))
 
 
-def _elsewhere(fn, t, stream, used, *args):
-    """fn(*args) with the device of t current and, if given, on `stream`: what the
-    call allocates belongs to that stream, and what it uses is kept for it."""
+def _elsewhere(fn, stream, *args):
+    """fn(*args) with the first tensor's device current and, if given, on `stream`: what
+    the call allocates belongs to that stream, and what it uses is kept for it."""
+    t = args[0][0] if isinstance(args[0], tuple) and args[0] else args[0]
+    if not isinstance(t, torch.Tensor):
+        raise MoEError(1, f"{fn.__name__}: the first argument must hold tensors, not {type(t).__name__}")
     dev = t.device
     if dev.type != "cuda":
         raise MoEError(1, f"{fn.__name__}: the tensors must be CUDA tensors, not on {dev}")
@@ -64,13 +67,14 @@ def _elsewhere(fn, t, stream, used, *args):
             return fn(*args)
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, dev) if stream else torch.cuda.default_stream(dev)
-        if stream.device != dev:
-            raise MoEError(1, f"{fn.__name__}: the stream is of {stream.device}, the tensors of {dev}")
+        if getattr(stream, "device", None) != dev:
+            raise MoEError(1, f"{fn.__name__}: the tensors are on {dev}, {stream} is no stream of it")
         with torch.cuda.stream(stream):
             got = fn(*args)
-            for t in used:
-                if t is not None:
-                    t.record_stream(stream)
+            for a in args:
+                for t in a if isinstance(a, tuple) else (a,):
+                    if isinstance(t, torch.Tensor):
+                        t.record_stream(stream)
             return got
 
 
@@ -86,7 +90,7 @@ def fp4_quantize(x, fmt="mxfp4", rows_per_scale=None, out=None, stream=None):
         got = _ops.fp4_quantize(x, fmt, rows_per_scale, out)
         if got is not None:
             return got
-    return _elsewhere(fp4_quantize, x, stream, (x,) if out is None else (x, *out[:3]), x, fmt, rows_per_scale, out)
+    return _elsewhere(fp4_quantize, stream, x, fmt, rows_per_scale, out)
 
 
 def fp4_dequantize(q, dtype=torch.float32, out=None, stream=None):
@@ -97,7 +101,7 @@ def fp4_dequantize(q, dtype=torch.float32, out=None, stream=None):
         got = _ops.fp4_dequantize(q, dtype, out)
         if got is not None:
             return got
-    return _elsewhere(fp4_dequantize, q[0], stream, (*q[:3], out), q, dtype, out)
+    return _elsewhere(fp4_dequantize, stream, q, dtype, out)
 
 
 def fp4_matmul(x, w, offsets=None, out_dtype=torch.bfloat16, out=None, stream=None):
@@ -114,7 +118,7 @@ def fp4_matmul(x, w, offsets=None, out_dtype=torch.bfloat16, out=None, stream=No
         got = _ops.fp4_matmul(x, w, offsets, out_dtype, out)
         if got is not None:
             return got
-    return _elsewhere(fp4_matmul, x[0], stream, (*x[:3], *w[:3], offsets, out), x, w, offsets, out_dtype, out)
+    return _elsewhere(fp4_matmul, stream, x, w, offsets, out_dtype, out)
 
 
 # ----------------------------------------------------------------- expert rows
@@ -126,7 +130,7 @@ def sort_tokens(ids, n_experts, stream=None):
         got = _ops.sort_tokens(ids, n_experts)
         if got is not None:
             return got
-    return _elsewhere(sort_tokens, ids, stream, (ids,), ids, n_experts)
+    return _elsewhere(sort_tokens, stream, ids, n_experts)
 
 
 def dispatch(x, inv, rows=None, out=None, stream=None):
@@ -137,7 +141,7 @@ def dispatch(x, inv, rows=None, out=None, stream=None):
         got = _ops.dispatch(x, inv, rows, out)
         if got is not None:
             return got
-    return _elsewhere(dispatch, x, stream, (x, inv, out), x, inv, rows, out)
+    return _elsewhere(dispatch, stream, x, inv, rows, out)
 
 
 def dispatch_backward(dxs, inv, out=None, stream=None):
@@ -146,7 +150,7 @@ def dispatch_backward(dxs, inv, out=None, stream=None):
         got = _ops.dispatch_backward(dxs, inv, out)
         if got is not None:
             return got
-    return _elsewhere(dispatch_backward, dxs, stream, (dxs, inv, out), dxs, inv, out)
+    return _elsewhere(dispatch_backward, stream, dxs, inv, out)
 
 
 def combine(ys, inv, gates=None, out_dtype=None, out=None, stream=None):
@@ -156,7 +160,7 @@ def combine(ys, inv, gates=None, out_dtype=None, out=None, stream=None):
         got = _ops.combine(ys, inv, gates, out_dtype, out)
         if got is not None:
             return got
-    return _elsewhere(combine, ys, stream, (ys, inv, gates, out), ys, inv, gates, out_dtype, out)
+    return _elsewhere(combine, stream, ys, inv, gates, out_dtype, out)
 
 
 def combine_backward(dy, ys, inv, gates=None, out=None, stream=None):
@@ -167,4 +171,4 @@ def combine_backward(dy, ys, inv, gates=None, out=None, stream=None):
         got = _ops.combine_backward(dy, ys, inv, gates, out)
         if got is not None:
             return got
-    return _elsewhere(combine_backward, dy, stream, (dy, ys, inv, gates, out), dy, ys, inv, gates, out)
+    return _elsewhere(combine_backward, stream, dy, ys, inv, gates, out)

@@ -221,3 +221,19 @@ def test_a_binding_of_another_torch_or_python_is_built_again(F, tmp_path, monkey
     os.remove(b.SO_BINDING)
     b.build_binding()
     assert len(made) == 4
+
+
+def test_arguments_of_another_kind_are_refused_beside_a_stream_too(F):
+    """The detour of calls with stream= looks at the arguments before the compiled check does."""
+    import torch
+    x, ids = torch.zeros((4, 64)), torch.zeros((4, 2), dtype=torch.int32)
+    for stream in (None, 0, 1):
+        for call in (lambda s: F.fp4_quantize("x", stream=s), lambda s: F.fp4_dequantize(None, stream=s),
+                     lambda s: F.fp4_dequantize((), stream=s), lambda s: F.fp4_matmul(None, None, stream=s),
+                     lambda s: F.fp4_matmul(x, None, stream=s), lambda s: F.fp4_matmul((None,) * 4, 7, stream=s),
+                     lambda s: F.sort_tokens([1, 2], 4, stream=s), lambda s: F.dispatch(None, ids, stream=s),
+                     lambda s: F.dispatch_backward(3, ids, stream=s), lambda s: F.combine("x", ids, stream=s),
+                     lambda s: F.combine_backward(None, x, ids, stream=s), lambda s: F.fp4_quantize(x, out=3, stream=s)):
+            with pytest.raises(F.MoEError) as ei:
+                call(stream)
+            assert ei.value.status == 1
