@@ -119,7 +119,7 @@ def lib():
         L.moe_fp4_quantize.argtypes = [p, i32, i64, i64, i64, i32, i64, p, p, p, p]
         L.moe_fp4_dequantize.argtypes = [p, p, p, i32, i64, i64, i64, p, i32, i64, p]
         L.moe_fp4_matmul.argtypes = [p, p, p, i32, p, p, p, i32, i32, i32, i32, p, p, i32, i64, p]
-        L.moe_debug_give_up.argtypes = [p]
+        L.moe_debug_give_up.argtypes = [i32, p]
         L.moe_sort_tokens.argtypes = [p, i32, i32, i32, p, p, p, p, p]
         L.moe_dispatch.argtypes = [p, i32, i32, i32, i32, i64, p, i32, p, i64, p]
         L.moe_dispatch_backward.argtypes = [p, i32, i32, i32, i32, i32, i64, p, p, i64, p]

@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
           if (lane < m.nrows) f = wG * __ldg(a.xG + m.row0 + lane);
           far = !__all_sync(0xffffffffu, whole_factor(f));
         }
-        if (!mm_wait_warp(smem_u32(&accf_bar[buf]), (n / NBUF) & 1, &gave_up, a.err, 64)) break;
+        if (!mm_wait_warp(smem_u32(&accf_bar[buf]), (n / NBUF) & 1, &gave_up, a.err, 64, k1 - k0)) break;
         tc_fence_after();
         const uint32_t acc = tmem + (uint32_t)(buf * NT) + ((uint32_t)(32 * quad) << 16);
         const int col = m.rb * 128 + 32 * quad + lane;
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp4_matmul_kernel(const __grid_
     bool ok = k1 > k0;                                     // a rank without stages adds nothing
     const float wG = (WF == WF_NV && any) ? __ldg(a.wG + m.g) : 1.0f;       // on their way while the products end
     if (WF == WF_NV && any && tid < m.nrows) xG_s[tid] = __ldg(a.xG + m.row0 + tid);
-    if (any && warp >= 2 && warp < 6) ok = mm_wait_warp(smem_u32(&accf_bar[0]), 0, &gave_up, a.err, 66) && ok;
+    if (any && warp >= 2 && warp < 6) ok = mm_wait_warp(smem_u32(&accf_bar[0]), 0, &gave_up, a.err, 66, k1 - k0) && ok;
     __syncwarp();
     cluster_wait();                                        // every rank has begun (long ago)
     const int plog = 7 - rlog, per = 1 << plog;
@@ -396,8 +396,8 @@ moe_status_t matmul_take_error(const char *fn) {
   return ops_fail(MOE_ERR_CUDA, fn, "a device-side wait of an earlier call gave up (code " + std::to_string(code) + ")");
 }
 
-// A wait that nothing ends, as the kernels wait, for a millisecond.
-__global__ void __launch_bounds__(32) give_up_kernel(int *err) {
+// A wait that nothing ends, as the kernels wait, for a millisecond and what `stages` add.
+__global__ void __launch_bounds__(32) give_up_kernel(int *err, int stages) {
   __shared__ __align__(8) uint64_t bar;
   __shared__ int gave_up;
   if (threadIdx.x == 0) {
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(32) give_up_kernel(int *err) {
     mbar_fence_init();
   }
   __syncwarp();
-  mm_wait_warp(smem_u32(&bar), 0, &gave_up, err, 60, 1000000ull);
+  mm_wait_warp(smem_u32(&bar), 0, &gave_up, err, 60, stages, 1000000ull);
 }
 
 template <int WF, int NT, bool SPLIT>
@@ -575,10 +575,11 @@ extern "C" moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_
   return ops_launched(fn, e);
 }
 
-extern "C" moe_status_t moe_debug_give_up(void *stream) {
+extern "C" moe_status_t moe_debug_give_up(int32_t stages, void *stream) {
   static const char fn[] = "moe_debug_give_up";
+  if (stages < 0 || stages > 250000) return ops_invalid(fn, "stages must be 0 to 250000 (a second)");
   int *err = nullptr;
   if (const moe_status_t st = matmul_error_word(fn, &err); st != MOE_OK) return st;
-  give_up_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(err);
+  give_up_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(err, stages);
   return ops_launched(fn, cudaSuccess);
 }

@@ -36,7 +36,11 @@ struct MatmulArgs {
 // word, which the next call of the host reads.  Nothing that outlives the CTA is
 // polled: a launch that fails cannot end a wait of another launch, of its own next
 // replay, or of a CTA that works.
-__device__ __forceinline__ bool mm_wait(uint32_t bar, uint32_t parity, int *gave_up, int *err, int code,
+//
+// The limit is kWaitLimitNs, and 4 us more for each stage that is waited for: a wait for
+// an accumulator lasts as long as its item's K range, and 2^30 elements are 4 M stages of
+// some 0.4 us (100 groups of two rows each, N 1: 1.7 s).
+__device__ __forceinline__ bool mm_wait(uint32_t bar, uint32_t parity, int *gave_up, int *err, int code, int stages = 0,
                                         unsigned long long limit = kWaitLimitNs) {
   if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = global_ns();
@@ -44,7 +48,7 @@ __device__ __forceinline__ bool mm_wait(uint32_t bar, uint32_t parity, int *gave
     if (mbar_try_wait(bar, parity)) return true;
     if ((i & 255u) == 0) {
       if (*(volatile int *)gave_up != 0) return false;
-      if (global_ns() - t0 > limit) {
+      if (global_ns() - t0 > limit + 4000ull * (unsigned)stages) {
         *(volatile int *)gave_up = 1;
         *(volatile int *)err = code;
         __threadfence_system();
@@ -55,8 +59,8 @@ __device__ __forceinline__ bool mm_wait(uint32_t bar, uint32_t parity, int *gave
 }
 // The same by every lane of a warp, true only when it succeeded for all of them.
 __device__ __forceinline__ bool mm_wait_warp(uint32_t bar, uint32_t parity, int *gave_up, int *err, int code,
-                                             unsigned long long limit = kWaitLimitNs) {
-  return __all_sync(0xffffffffu, mm_wait(bar, parity, gave_up, err, code, limit));
+                                             int stages = 0, unsigned long long limit = kWaitLimitNs) {
+  return __all_sync(0xffffffffu, mm_wait(bar, parity, gave_up, err, code, stages, limit));
 }
 
 // ------------------------------------------------------------------ work items

@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_matmul_pair_kernel(const 
         }
         far = !__all_sync(0xffffffffu, whole_factor(xG[0]) && whole_factor(xG[1]) && whole_factor(xG[2]) && whole_factor(xG[3]));
       }
-      if (!mm_wait_warp(smem_u32(&accf_bar[buf]), (n >> 1) & 1, &gave_up, a.err, 74)) break;
+      if (!mm_wait_warp(smem_u32(&accf_bar[buf]), (n >> 1) & 1, &gave_up, a.err, 74, nk)) break;
       tc_fence_after();
       const uint32_t acc = tmem + (buf ? (uint32_t)(Geo::SF_TMEM - 32 * chunks) : 0u) + ((uint32_t)(32 * quad) << 16);
       if constexpr (WF == WF_NV) {

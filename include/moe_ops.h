@@ -84,12 +84,13 @@ moe_status_t moe_fp4_dequantize(const uint8_t *codes, const uint8_t *scales, con
  * K is a multiple of 32, 1 <= n_groups <= 1024; codes are 16-byte aligned and y
  * aligned to its type; rows <= 2^27; N and K <= 2^30; n_groups * N below 2^31.  The scale rows
  * are read fastest when they start on 16 bytes (K a multiple of 512, with NVFP4 of
- * 256).  Every wait inside the kernel is bounded.  Should one give up, that launch's y
- * is invalid, and that launch's alone: whatever else is queued, runs beside it or
- * replays it later is right.  The first moe_fp4_matmul on the device that begins
- * after that returns MOE_ERR_CUDA, having enqueued nothing; one such return covers every
- * failure up to it, and the calls after it run.  A replay of a captured product is no call: a
- * program that only replays asks with a call of rows = 0, which enqueues nothing. */
+ * 256).  Every wait inside the kernel is bounded, by two seconds and more where rows are
+ * very long.  Should one give up, that launch's y is invalid, and that launch's alone:
+ * whatever else is queued, runs beside it or replays it later is right.  The first
+ * moe_fp4_matmul on the device that begins after that returns MOE_ERR_CUDA, having
+ * enqueued nothing; one such return covers every failure up to it, and the calls after it
+ * run.  A replay of a captured product is no call: a program that only replays asks with
+ * a call of rows = 0, which enqueues nothing. */
 moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_scales, const float *x_global, int32_t rows,
                             const uint8_t *w_codes, const uint8_t *w_scales, const float *w_global, int32_t n_groups,
                             int32_t N, int32_t K, int32_t fmt, const int32_t *offsets, void *y, int32_t dtype,
@@ -97,8 +98,10 @@ moe_status_t moe_fp4_matmul(const uint8_t *x_codes, const uint8_t *x_scales, con
 
 /* Test hook, beside moe_debug_inject: enqueue a kernel whose one wait, on a barrier
  * that nothing completes, gives up after a millisecond, as a wait of moe_fp4_matmul
- * does at its limit.  Causes no GPU fault and writes nothing but the error. */
-moe_status_t moe_debug_give_up(void *stream);
+ * does at its limit of two seconds.  To both come 4 us for each of `stages` stages of 256
+ * elements that are waited for (here 0 to 250000).  Causes no GPU fault and writes
+ * nothing but the error. */
+moe_status_t moe_debug_give_up(int32_t stages, void *stream);
 
 /* Sort the T * k pairs p = t * k + j by their expert ids[p], ties by ascending p
  * (the order of moe_forward's routing).  An id outside [0, E), a sink target or

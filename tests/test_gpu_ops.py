@@ -846,7 +846,7 @@ def test_binding_refusals_on_the_gpu():
 # ------------------------------------------------- products after a wait that gave up
 def _give_up(F, stream=None):
     s = G.torch().cuda.current_stream() if stream is None else stream
-    assert F.lib().moe_debug_give_up(s.cuda_stream) == 0
+    assert F.lib().moe_debug_give_up(0, s.cuda_stream) == 0
 
 
 def _reported_once(F, call):
@@ -1200,3 +1200,22 @@ def test_gradients_called_within_a_function_of_ones_own():
     # three fp32 roundings of xs^2 and its gradient, and the sums' own
     assert np.all(np.abs(f64(gates.grad) - dg) <= (H + 1) * 2.0 ** -24 * mag * (1 + 2.0 ** -20) + TINY["f32"])
     assert np.all(np.abs(f64(x.grad) - dx) <= (k + 4) * 2.0 ** -24 * dmag * (1 + 2.0 ** -20) + TINY["f32"])
+
+
+def test_a_wait_for_a_long_item_has_a_longer_limit():
+    """4 us a stage, ten times what one takes: no row that the product accepts is given up on."""
+    t, F = G.torch(), G.library()
+    _, w, off, _ = _small_products()[2]
+    none = F.fp4_quantize(t.empty((0, 512), device="cuda"), "nvfp4")
+    took = []
+    for stages in (0, 50000):
+        a, b = t.cuda.Event(enable_timing=True), t.cuda.Event(enable_timing=True)
+        a.record()
+        assert F.lib().moe_debug_give_up(stages, t.cuda.current_stream().cuda_stream) == 0
+        b.record()
+        t.cuda.synchronize()
+        took.append(a.elapsed_time(b))
+        _reported_once(F, lambda: F.fp4_matmul(none, w, off))
+    # the limit is a time of the GPU's own clock, read every 256 polls: not before it, and soon after
+    assert 0.99 <= took[0] < 100 and 200 <= took[1] < 400, took
+    assert F.lib().moe_debug_give_up(-1, None) == 1 and F.lib().moe_debug_give_up(250001, None) == 1
