@@ -84,7 +84,8 @@ inline cudaError_t launch_op(void (*fn)(Args...), dim3 grid, int block, size_t s
   return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
-// Division of numbers below 2^31 by one that is known at launch: a multiplication
+// Division of numbers below 2^31 by one that is known at launch (Granlund and
+// Montgomery 1994): a multiplication
 // by m = ceil(2^(31 + l) / d), l = ceil(log2 d), is exact there (the hardware's own
 // 32-bit division takes three turns of the slow conversion pipe).
 struct FastDiv {

@@ -4,7 +4,8 @@
 //   NVFP4, block of 16:  G = 2^ceil(log2(amax_group / 2688)),  s = RNE_E4M3(amax / (6 G)),
 //                        c = RNE(v / (s G))
 //
-// Every rounding is that of the real quotient, with no double rounding:
+// Every rounding to codes and scales is that of the real quotient, with no double
+// rounding (the way back has its own section below):
 //  * 2^X is a power of two: v * 2^-X is exact.
 //  * The borders between codes, and between scales, have few digits: times d = s G
 //    (4 digits) or 6 G they are fp32 numbers, so a quotient that is not on a border
@@ -21,11 +22,13 @@
 // Bound by memory: x is read once and 0.53 or 0.56 bytes an element are written.
 // A thread takes pieces of 16 consecutive elements (one NVFP4 block, half an MXFP4
 // block), 32 bytes of 16-bit elements in one access.  8192 x 4096 bf16: MXFP4 13.8
-// us quantised, 13.6 read back (94% and 95% of the copy rate); NVFP4 by rows 15.8
-// and 15.0 (83%, 88%): there the arithmetic, some 100 instructions a piece, shows.
+// us quantised, 13.6 read back (94% and 95% of the copy rate); NVFP4 by rows 15.7
+// and 14.6 (83%, 90%): there the arithmetic, some 150 instructions a piece, shows.
 // An NVFP4 scale over many rows needs a pass over x before the codes: 64 matrices of
-// 1024 x 2048 98.3 us, of 93 for the two reads (a cluster a matrix, to read it again
-// from L2, takes 97 to 147).
+// 1024 x 2048 97.6 us (53% of the copy rate for x once and the codes), of 93 for the two
+// reads and the codes (a cluster a matrix, to read it again from L2, takes 97 to 147).
+#include <type_traits>
+
 #include "ops_common.cuh"
 
 namespace moe {
@@ -319,8 +322,9 @@ __global__ void __launch_bounds__(256) group_scale_kernel(const FpArgs a, uint32
 // a border between two 16-bit numbers: seldom, and never where G is a power of two.  A
 // piece that has such a border in it (Borders) is done again with fp32 products rounded
 // to odd (towards zero, the last digit set where something was cut off), which stay on
-// their side of every border (Boldo and Melquiond 2008).  With every product rounded to
-// odd 8192 x 4096 to bf16 took 17.8 us.
+// their side of every border (Boldo and Melquiond 2008).  8192 x 4096 to bf16, with all
+// in L2: 12.9 us, with any G 12.8, with every product rounded to odd 17.8; to f16 13.5, and
+// 26 where all values are below 2^-9 and G has more than 18 digits (small() below).
 template <typename T>
 struct Borders {
   uint32_t least = 0xFFFFFFFFu;                            // two at a time: 0 where one was met

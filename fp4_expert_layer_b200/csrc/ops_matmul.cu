@@ -19,8 +19,8 @@
 // few items (SPLIT) a cluster of CTAs shares an item's K range and adds the parts in
 // rank order through distributed shared memory.
 //
-// Measured: 256 rows over 64 groups, N = K = 2048, NVFP4: 29.4 us, 5.1 TB/s (some 3
-// us of it are the way to the first stage); 1 row, N = K = 4096, MXFP4: 5.8 us, of
+// Measured, from a graph: 256 rows over 64 groups, N = K = 2048, NVFP4: 29.0 us, 5.2 TB/s (some 3
+// us of it are the way to the first stage); 1 row, N = K = 4096, MXFP4: 5.6 us, of
 // which the weights need 1.4 and the way through launch, first stage and the
 // cluster's meeting the rest.
 //

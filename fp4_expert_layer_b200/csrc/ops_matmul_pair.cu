@@ -9,11 +9,11 @@
 // then bound by this fill, L2 to shared memory (some 50 bytes a clock an SM), at half
 // of what the tensor pipe does.
 //
-// Measured: 8192 x 4096 x 4096, MXFP4, fp32 result 63.4 us (4.3 PFLOP/s; the MMAs
-// alone, with no operand copied, 51.7; under a second of load the power cap takes
-// the clock to 1.7 GHz and the time to 74); 16384 rows over 128 groups, N 1536, K
-// 2048, NVFP4, bf16 66.0 us (4.5 TB/s, of 45 us for its bytes).  One CTA a 128 x 128
-// tile took 120 and 151.
+// Measured, 20 launches from a graph: 8192 x 4096 x 4096, MXFP4, fp32 result 61.2 to 63 us
+// (4.4 PFLOP/s; the MMAs alone, with no operand copied, 51.7); 16384 rows over 128 groups,
+// N 1536, K 2048, NVFP4, bf16 66.2 us (4.5 TB/s, of 45 us for its bytes).  Called in a row
+// for a second the power cap takes the clock to 1.7 GHz and the times to 74 and 75.  One
+// CTA a 128 x 128 tile took 120 and 151.
 //
 // The MMA is as wide as the item has rows (rounded up to 32), and boxes of 64 rows
 // that it does not need are not copied, so a ragged segment costs what it holds.

@@ -252,7 +252,9 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) 
 // in this thread's own CTA (shared memory behind fence.proxy.async, TMEM behind a
 // tcgen05 fence): the barrier orders the issue, no thread of the other CTA reads
 // the data, so the release has CTA scope.  With cluster scope each arrival costs
-// 0.8 us, more than a stage of MMAs.
+// 0.8 us, more than a stage of MMAs.  PTX's memory model does not promise the order at
+// CTA scope, since another CTA's thread issues the reads; it is the form in which CTA
+// pairs are commonly fed, and results repeat bit for bit.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
