@@ -1219,3 +1219,48 @@ def test_a_wait_for_a_long_item_has_a_longer_limit():
     # the limit is a time of the GPU's own clock, read every 256 polls: not before it, and soon after
     assert 0.99 <= took[0] < 100 and 200 <= took[1] < 400, took
     assert F.lib().moe_debug_give_up(-1, None) == 1 and F.lib().moe_debug_give_up(250001, None) == 1
+
+
+@pytest.mark.parametrize("out, pad", [("f32", 0), ("bf16", 0), ("bf16", 3)])
+@pytest.mark.parametrize("which", ["every third", "chunks", "one"])
+def test_distant_scales_in_tiles_of_many_rows(which, out, pad):
+    """Both ends of the accumulators, several items a pair, chunks with and without such rows."""
+    t, F = G.torch(), G.library()
+    lens, N, K = [1300, 0, 257, 256, 1, 95, 900], 2100, 288
+    rows, E = sum(lens), len(lens)
+    x, w = _operands("nvfp4", rows, E, N, K, 500)
+    rng = np.random.default_rng(5)
+    for q in (x, w):
+        q.scales.copy_(t.from_numpy(rng.integers(112, 127, tuple(q.scales.shape), dtype=np.uint8)))
+    r = t.arange(rows, device="cuda")
+    far = {"every third": r % 3 == 0, "chunks": r % 64 < 32, "one": r == 1400}[which]
+    w.global_scale.fill_(1.9 * 2.0 ** -80)
+    x.global_scale.copy_(t.where(far, 1.1 * 2.0 ** -75, 1.3 * 2.0 ** 70))
+    off = t.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=t.int32, device="cuda")
+    y0 = randn((rows, N), 1, out)
+    y = placed(y0, pad, 0)
+    F.fp4_matmul(x, w, off, out=y)
+    _check_product(x, w, off, y0, y, out)
+    again = placed(y0, pad, 0)
+    F.fp4_matmul(x, w, off, out=again)
+    assert t.equal(y, again)
+
+
+@pytest.mark.parametrize("out, pad, shift", [("bf16", 8, 8), ("bf16", 3, 1), ("f16", 8, 0), ("f16", 1, 1), ("f32", 3, 1)])
+def test_dequantize_rounds_once_into_rows_at_any_element(out, pad, shift):
+    t, F = G.torch(), G.library()
+    n, K = 700, 544
+    rng = np.random.default_rng(9)
+    codes = rng.integers(0, 256, (n, K // 2), dtype=np.uint8)
+    scales = rng.integers(0, 127, (n, K // 16), dtype=np.uint8)
+    Gs = (rng.uniform(0.5, 2, n) * 2.0 ** rng.integers(-20, 6, n)).astype(np.float32)
+    # on a border of bf16, and of f16, but for the last digits: 1.5 (1 + 2^-8) / 1.5 and the like
+    Gs[::5] = np.float32(1 + 2.0 ** -8) + np.float32(2.0 ** -23) * rng.integers(-2, 3, Gs[::5].size).astype(np.float32)
+    Gs[1::5] = np.float32(1 + 2.0 ** -11) + np.float32(2.0 ** -23) * rng.integers(-2, 3, Gs[1::5].size).astype(np.float32)
+    q = F.FP4Tensor(t.from_numpy(codes).cuda(), t.from_numpy(scales).cuda(), t.from_numpy(Gs).cuda(), "nvfp4")
+    o = placed(t.full((n, K), 7.0, dtype=dt(out), device="cuda"), pad, shift)
+    F.fp4_dequantize(q, out=o)
+    assert np.array_equal(f64(o), _nearest(ref.values(codes, scales, Gs, "nvfp4"), out))
+    if pad:
+        whole = t.as_strided(o, (n - 1, pad), (K + pad, 1), o.storage_offset() + K)
+        assert (whole == 0).all()                          # what lies between the rows is not touched
